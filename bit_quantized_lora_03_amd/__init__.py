@@ -41,3 +41,17 @@ from ._lib import (  # noqa: F401
     quantize_weight_centred,
     workspace_bytes,
 )
+
+# The 4-bit serving calls live in ``u4``, which needs torch; the rest of the
+# package does without until a call is made, so they are imported on first use.
+_U4 = ("Kv4Cache", "U4Weight", "dequantize_u4", "kv4_append", "kv4_attention",
+       "kv4_attention_workspace_bytes", "kv4_read", "linear_u4_fwd", "quantize_u4")
+
+
+def __getattr__(name):
+    if name in _U4:
+        from . import u4
+        for n in _U4:
+            globals()[n] = getattr(u4, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -32,7 +32,12 @@ EXPORTS = ("qlora_quantize_nf4", "qlora_double_quant", "qlora_quantize_nf4_dq",
            "qlora_dropout_keep_mask", "qlora_linear_fwd_dropout_rng",
            "qlora_linear_bwd_dropout_rng",
            "qlora_merge_adapter", "qlora_linear_fwd_noalloc", "qlora_nf4_levels",
-           "qlora_nf4_thresholds", "qlora_status_string")
+           "qlora_nf4_thresholds", "qlora_status_string",
+           "qlora_quantize_u4", "qlora_dequantize_u4", "qlora_dequantize_u4_f16",
+           "qlora_linear_u4_fwd", "qlora_linear_u4_fwd_f16",
+           "qlora_kv4_append", "qlora_kv4_append_f16", "qlora_kv4_read", "qlora_kv4_read_f16",
+           "qlora_kv4_attention_workspace_bytes", "qlora_kv4_attention",
+           "qlora_kv4_attention_f16")
 
 
 class QloraError(RuntimeError):
@@ -50,6 +55,28 @@ class Nf4Weight(ctypes.Structure):
                 ("dq_mean", ctypes.c_void_p)]
 
 
+class U4Struct(ctypes.Structure):
+    """``qlora_u4_weight``."""
+    _fields_ = [("codes", ctypes.c_void_p), ("pairs", ctypes.c_void_p), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("group", ctypes.c_int32)]
+
+
+class Kv4CacheStruct(ctypes.Structure):
+    """``qlora_kv4_cache``."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_pairs", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_pairs", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class Kv4BatchStruct(ctypes.Structure):
+    """``qlora_kv4_batch``."""
+    _fields_ = [("cu_q", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("seqs", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("max_q", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -65,6 +92,10 @@ def lib() -> ctypes.CDLL:
     vp, i64, i32, f32, sz, u64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                                   ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64)
     wp = ctypes.POINTER(Nf4Weight)
+    up, cp, bp = (ctypes.POINTER(U4Struct), ctypes.POINTER(Kv4CacheStruct),
+                  ctypes.POINTER(Kv4BatchStruct))
+    append = [cp, bp, vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, vp, i64, i32, i32, vp, vp]
+    attend = [cp, bp, vp, i64, i64, i32, f32, i32, i32, i64, vp, vp, vp, sz, vp]
     sig = {
         "qlora_quantize_nf4": ([vp, i64, i32, vp, vp, vp], ctypes.c_int),
         "qlora_double_quant": ([vp, i64, i32, vp, vp, vp], ctypes.c_int),
@@ -100,6 +131,18 @@ def lib() -> ctypes.CDLL:
         "qlora_nf4_levels": ([vp], ctypes.c_int),
         "qlora_nf4_thresholds": ([vp], ctypes.c_int),
         "qlora_status_string": ([ctypes.c_int], ctypes.c_char_p),
+        "qlora_quantize_u4": ([vp, i64, i32, vp, vp, vp], ctypes.c_int),
+        "qlora_dequantize_u4": ([up, vp, vp], ctypes.c_int),
+        "qlora_dequantize_u4_f16": ([up, vp, vp], ctypes.c_int),
+        "qlora_linear_u4_fwd": ([up, vp, i64, i64, vp, i64, vp], ctypes.c_int),
+        "qlora_linear_u4_fwd_f16": ([up, vp, i64, i64, vp, i64, vp], ctypes.c_int),
+        "qlora_kv4_append": (append, ctypes.c_int),
+        "qlora_kv4_append_f16": (append, ctypes.c_int),
+        "qlora_kv4_read": ([cp, bp, vp, vp, vp], ctypes.c_int),
+        "qlora_kv4_read_f16": ([cp, bp, vp, vp, vp], ctypes.c_int),
+        "qlora_kv4_attention_workspace_bytes": ([i64, i64, i64, i32, i32, i32, i32], sz),
+        "qlora_kv4_attention": (attend, ctypes.c_int),
+        "qlora_kv4_attention_f16": (attend, ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -527,13 +570,17 @@ def linear_bf16_bwd(W, x, dy, A, B, alpha: float, need_dx: bool = True, dA=None,
 
 
 def merge_adapter(base, A, B, alpha: float, out_f32: bool = True, out_bf16: bool = True,
-                  requantize: bool = False):
+                  requantize=False):
     """W_m = W_base + (alpha/r).B.A for export.  ``base`` is a PackedWeight
     (merge into the decoded 4-bit base) or an fp32 [N, K] device tensor (the
     original weights).  Returns ``(fp32 [N, K] or None, bf16 bits [N, K]
-    (int16) or None, PackedWeight or None)``; the last is the fp32 merge
-    quantised again (``requantize=True``; needs the fp32 output)."""
+    (int16) or None, PackedWeight, U4Weight or None)``; the last is the fp32
+    merge quantised again (needs the fp32 output): to NF4 with
+    ``requantize=True``, to the 4-bit group format (groups of 64) with
+    ``requantize="u4"``."""
     torch = _torch()
+    if isinstance(requantize, str) and requantize != "u4":
+        raise ValueError(f"requantize: True, False or 'u4', not {requantize!r}")
     if requantize and not out_f32:
         raise ValueError("requantize needs the fp32 merge")
     packed = isinstance(base, PackedWeight)
@@ -550,5 +597,8 @@ def merge_adapter(base, A, B, alpha: float, out_f32: bool = True, out_bf16: bool
                                     None if packed else base.data_ptr(), N, K, _ptr(A),
                                     _ptr(B), r, float(alpha), _ptr(f), _ptr(b),
                                     _stream_ptr()), "qlora_merge_adapter")
+    if requantize == "u4":
+        from .u4 import quantize_u4
+        return f, b, quantize_u4(f)
     q = quantize_weight(f) if requantize else None
     return f, b, q

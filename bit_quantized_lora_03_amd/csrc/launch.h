@@ -182,4 +182,73 @@ hipError_t launch_merge(const uint8_t* codes, const uint8_t* qscale, const float
                         float scale, float* out_f32, uint16_t* out_bf16, int64_t N, int64_t K,
                         const Nf4Levels& L, hipStream_t s);
 
+// u4_quant.hip -- the 4-bit group format (u4_common.h): groups of 32, 64 or
+// 128 values, codes two per byte and one (s, m) pair per group; n a
+// multiple of the group
+hipError_t launch_quantize_u4(const float* w, int64_t n, int group, uint8_t* codes,
+                              uint32_t* pairs, hipStream_t s);
+hipError_t launch_dequantize_u4(const uint8_t* codes, const uint32_t* pairs, int64_t n, int group,
+                                uint16_t* out, bool f16, hipStream_t s);
+
+// u4_linear.hip -- y [M, N] = x [M, K] . W^T, rows of x and y ldx and ldy apart
+hipError_t launch_linear_u4(const uint8_t* codes, const uint32_t* pairs, int group,
+                            const uint16_t* x, int64_t ldx, uint16_t* y, int64_t ldy, int64_t M,
+                            int64_t N, int64_t K, bool f16, hipStream_t s);
+
+// kv4_cache.hip, kv4_attention.hip -- the 4-bit paged cache.  Codes
+// [pages][kv heads][page size][head_dim / 2], pairs [pages][kv heads][page
+// size]; page size 2^page_log2, 16 to 1024; head_dim 64, 128 or 256.
+struct Kv4CacheArg {
+  uint8_t* k_codes;
+  uint32_t* k_pairs;
+  uint8_t* v_codes;
+  uint32_t* v_pairs;
+  int64_t pages;
+  int page_log2, kv_heads, head_dim;
+};
+// A ragged batch: sequence b has the rows cu_q[b] .. cu_q[b + 1] - 1 (at most
+// max_q, and T = rows in all), which are its last tokens of seq_lens[b].
+struct Kv4BatchArg {
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  const int32_t* block_table;  // [seqs][table_width]
+  int64_t rows;
+  int seqs, table_width, max_q;
+};
+// Strides in elements: ts from token to token, hs from head to head.
+struct Kv4AppendArg {
+  const uint16_t *q, *k, *v;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+  const float* cos_sin;  // [table_rows][rot]: cosines, then sines
+  int64_t table_rows;
+  int q_heads, rot, interleaved;  // q_heads 0: no queries
+  uint16_t* q_out;                // [T][q_heads][head_dim]
+};
+hipError_t launch_kv4_append(const Kv4CacheArg& c, const Kv4BatchArg& b, const Kv4AppendArg& a,
+                             bool f16, hipStream_t s);
+hipError_t launch_kv4_read(const Kv4CacheArg& c, const Kv4BatchArg& b, uint16_t* k_out,
+                           uint16_t* v_out, bool f16, hipStream_t s);
+
+struct Kv4AttnArg {
+  const uint16_t* q;
+  int64_t q_ts, q_hs;
+  int q_heads;
+  float scale;
+  int causal, window;  // window 0: none
+  int64_t table_keys;  // tokens the block table has room for, at most 2^30
+  uint16_t* out;  // [T][q_heads][head_dim]
+  float* lse;     // [T][q_heads], or null
+};
+// How a call is cut: tiles of `tile` query rows, and the axis of the keys in
+// chunks of `chunk` tokens (splits of them for the longest sequence; 1:
+// no partial results).
+struct Kv4AttnPlan {
+  int tile, tiles, chunk, splits;
+};
+Kv4AttnPlan kv4_attn_plan(int64_t seqs, int64_t max_q, int64_t max_len, int q_heads, int kv_heads,
+                          int head_dim, int window);
+size_t kv4_attn_workspace(const Kv4AttnPlan& p, int64_t seqs, int kv_heads, int head_dim);
+hipError_t launch_kv4_attention(const Kv4CacheArg& c, const Kv4BatchArg& b, const Kv4AttnArg& a,
+                                const Kv4AttnPlan& p, float* workspace, bool f16, hipStream_t s);
+
 }  // namespace qlora

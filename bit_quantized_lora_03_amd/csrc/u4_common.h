@@ -1,0 +1,154 @@
+// The 4-bit group format: a group of G values holds a code c in 0..15 for
+// each and one pair (s, m) of bf16; a value is m + s c.  Codes are packed
+// two per byte, the even element in the low nibble; a pair is one 32-bit
+// word, s in the low half.
+#pragma once
+
+#include "device_common.h"
+
+namespace qlora {
+
+// ---- encoding --------------------------------------------------------------
+// m = the group's minimum rounded down to bf16, s = (maximum - m) / 15
+// rounded up to bf16, c = rint((v - m) / s) with ties to even (0 where s is
+// 0), all as computed in fp64.  Rounding m down and s up keeps every
+// (v - m) / s inside [0, 15], so no code is clipped and a value is off by at
+// most s / 2.  A group that holds a NaN or an infinity, or whose m or s
+// passes bf16's range, gets m = s = NaN and codes 0: whatever reads it is
+// NaN too.
+
+// The largest bf16 value not above x, as fp32 bits.
+__device__ __forceinline__ uint32_t bf16_down(double x) {
+  const uint32_t b = __float_as_uint(__double2float_rd(x));
+  const uint32_t low = b & 0xFFFFu;
+  return b - low + ((low && (b >> 31)) ? 0x10000u : 0u);
+}
+// The smallest bf16 value not below x, as fp32 bits.
+__device__ __forceinline__ uint32_t bf16_up(double x) {
+  const uint32_t b = __float_as_uint(__double2float_ru(x));
+  const uint32_t low = b & 0xFFFFu;
+  return b - low + ((low && !(b >> 31)) ? 0x10000u : 0u);
+}
+
+struct U4Coder {
+  float s, m;
+  float inv;    // fp32 1 / s, or 0 where the exact quotient has to be taken
+  uint32_t pair;
+};
+
+// finite: every value of the group is finite
+__device__ __forceinline__ U4Coder u4_coder(double lo, double hi, bool finite) {
+  U4Coder u;
+  u.m = __uint_as_float(bf16_down(lo));
+  u.s = __uint_as_float(bf16_up((hi - (double)u.m) / 15.0));
+  // also false for an infinite or NaN m or s
+  finite = finite && fabsf(u.m) <= 3.4e38f && fabsf(u.s) <= 3.4e38f;
+  if (!finite) u.s = u.m = __uint_as_float(0x7FC00000u);
+  // below 2^-100 the fp32 reciprocal nears its range: take the exact path
+  u.inv = u.s > 0x1p-100f ? 1.0f / u.s : 0.0f;
+  u.pair = (__float_as_uint(u.s) >> 16) | (__float_as_uint(u.m) & 0xFFFF0000u);
+  return u;
+}
+
+// rint((v - m) / s), t = fp32(v - m).  The fp32 quotient t * inv is within
+// 15 * 2^-22 (t, inv and the product are each rounded once) of the exact
+// one, so it decides the code wherever it lies further than 1e-4 from a
+// half; the few others (about one in 5000) divide in fp64.
+__device__ __forceinline__ uint32_t u4_code(const U4Coder& u, double v, float t) {
+  const float q = t * u.inv;
+  float c = rintf(q);
+  if (!(fabsf(q - c) < 0.4999f) || u.inv == 0.0f)
+    c = u.s > 0.0f ? (float)rint((v - (double)u.m) / (double)u.s) : 0.0f;
+  return (uint32_t)fminf(fmaxf(c, 0.0f), 15.0f);  // a NaN becomes 0
+}
+
+// ---- decoding --------------------------------------------------------------
+// Products read the codes as 16-bit floats OFF + c, formed by putting the
+// code into the mantissa of a constant: two codes per v_and_or_b32 and no
+// conversion.  The offset leaves through sum(x (OFF + c)) - OFF sum(x),
+// which costs bits of the fp32 sum (7 at OFF = 128, 4 at 16): bf16, whose
+// 7-bit mantissa ends at the code with OFF = 128, rounds its operands far
+// above that; fp16 shifts the code to the mantissa's top, where OFF is 16.
+// The pairs of a word are (element j, element j + 4), j = 0..3.
+template <class DT>
+struct U4Mfma;
+template <>
+struct U4Mfma<Bf16T> {
+  static constexpr float kOff = 128.0f;
+  static constexpr uint32_t kOne = 0x3F803F80u;  // two ones
+  static __device__ __forceinline__ uint32_t pair(uint32_t w, int j) {
+    return ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+  }
+};
+template <>
+struct U4Mfma<F16T> {
+  static constexpr float kOff = 16.0f;
+  static constexpr uint32_t kOne = 0x3C003C00u;
+  static __device__ __forceinline__ uint32_t pair(uint32_t w, int j) {
+    const int sh = 6 - 4 * j;
+    return ((sh > 0 ? w << sh : w >> -sh) & 0x03C003C0u) | 0x4C004C00u;
+  }
+};
+// The 8 codes of a word as MFMA operand, in the order 0 4 1 5 2 6 3 7.
+template <class DT>
+__device__ __forceinline__ u32x4_t u4_expand8(uint32_t w) {
+  return u32x4_t{U4Mfma<DT>::pair(w, 0), U4Mfma<DT>::pair(w, 1), U4Mfma<DT>::pair(w, 2),
+                 U4Mfma<DT>::pair(w, 3)};
+}
+// Eight 16-bit values in the same order.
+__device__ __forceinline__ u32x4_t u4_order8(u32x4_t v) {
+  return u32x4_t{perm(v[2], v[0], 0x05040100u), perm(v[2], v[0], 0x07060302u),
+                 perm(v[3], v[1], 0x05040100u), perm(v[3], v[1], 0x07060302u)};
+}
+__device__ __forceinline__ float u4_s(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float u4_m(uint32_t pair) {
+  return __uint_as_float(pair & 0xFFFF0000u);
+}
+// The 8 codes of a word as values m + s c (one rounding, to fp32).
+__device__ __forceinline__ void u4_values8(uint32_t w, uint32_t pair, float (&v)[8]) {
+  const float s = u4_s(pair), m = u4_m(pair);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fmaf(s, (float)((w >> (4 * i)) & 15u), m);
+}
+
+// ---- reductions over 8, 16 or 32 neighbouring lanes ------------------------
+// Each step brings every lane the value of a lane that holds the other half
+// of the lanes combined so far.
+template <int STEP>
+__device__ __forceinline__ float lane_other(float v) {
+  const int i = __float_as_int(v);
+  if constexpr (STEP == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0xB1, 15, 15, true));   // quad 1 0 3 2
+  if constexpr (STEP == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x4E, 15, 15, true));   // quad 2 3 0 1
+  if constexpr (STEP == 4) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x141, 15, 15, true));  // mirrored in 8
+  if constexpr (STEP == 8) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x140, 15, 15, true));  // mirrored in 16
+  return __shfl_xor(v, STEP);
+}
+template <int STEP>
+__device__ __forceinline__ double lane_other(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __float_as_uint(lane_other<STEP>(__uint_as_float((uint32_t)b)));
+  const uint32_t hi = __float_as_uint(lane_other<STEP>(__uint_as_float((uint32_t)(b >> 32))));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int LANES, class T>
+__device__ __forceinline__ void lanes_minmax(T& lo, T& hi) {
+  auto step = [&](T a, T b) {
+    lo = a < lo ? a : lo;
+    hi = b > hi ? b : hi;
+  };
+  if constexpr (LANES > 1) step(lane_other<1>(lo), lane_other<1>(hi));
+  if constexpr (LANES > 2) step(lane_other<2>(lo), lane_other<2>(hi));
+  if constexpr (LANES > 4) step(lane_other<4>(lo), lane_other<4>(hi));
+  if constexpr (LANES > 8) step(lane_other<8>(lo), lane_other<8>(hi));
+  if constexpr (LANES > 16) step(lane_other<16>(lo), lane_other<16>(hi));
+}
+// Whether `ok` holds in all of the LANES aligned lanes that the caller is in.
+template <int LANES>
+__device__ __forceinline__ bool lanes_all(bool ok) {
+  const uint64_t bad = __ballot(!ok);
+  const int first = (threadIdx.x & 63) & ~(LANES - 1);
+  constexpr uint64_t kMask = LANES == 64 ? ~0ull : (1ull << (LANES & 63)) - 1;
+  return ((bad >> first) & kMask) == 0;
+}
+
+}  // namespace qlora

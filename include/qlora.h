@@ -370,6 +370,162 @@ int qlora_linear_fwd_noalloc(const qlora_nf4_weight* w, const uint16_t* x, int64
                              const uint16_t* A, const uint16_t* B, int32_t r, float alpha,
                              uint16_t* y, void* stream);
 
+/* ---- 4-bit serving: group format, few-token product, paged cache ---------
+ * What a model needs next to the layer above once its adapter is merged and
+ * the merge is quantised again for serving ([QLoRA -- the democratization
+ * event, deployment note]): weights in a 4-bit format whose decode costs
+ * less than NF4's, and the other stream of a decode step, the keys and
+ * values, in the same format.  The pages give no such format; it is this
+ * library's reading.
+ *
+ * The 4-bit group format.  A group of values holds a code c in 0..15 for
+ * each (packed two per byte, even element in the low nibble) and one pair
+ * of bf16 (two uint16_t: s, then m); a value is m + s * c.
+ *   Encoding, as computed in fp64: m = the group's minimum rounded down to
+ *   bf16, s = (maximum - m) / 15 rounded up to bf16,
+ *   c = rint((v - m) / s) (half to even; 0 where s is 0).  No code is
+ *   clipped and |value - v| <= s / 2.
+ *   A group that holds a NaN or an infinity, or whose m or s passes bf16's
+ *   range, gets m = s = NaN and codes 0, and so decodes to NaN.  (These
+ *   calls take such inputs; those above do not check for them.)
+ * A weight [N, K] has groups of 32, 64 or 128 along K (4 + 32 / group bits
+ * per weight).  Device pointers, 16-byte aligned unless said otherwise.     */
+typedef struct qlora_u4_weight {
+  const uint8_t*  codes;  /* [N, K/2]            */
+  const uint16_t* pairs;  /* [N, K/group, 2]     */
+  int64_t         N;      /* 1 .. 2^30 - 1       */
+  int64_t         K;      /* a multiple of group, below 2^30 (ESHAPE) */
+  int32_t         group;  /* 32, 64 or 128 (ENOTSUP)                  */
+} qlora_u4_weight;
+
+/* fp32 w [n_elems] (a flattened [N, K] weight) to codes [n_elems/2] and
+ * pairs [n_elems/group, 2].  n_elems must be a multiple of group (ESHAPE)
+ * and may be 0 (nothing is enqueued).                                       */
+int qlora_quantize_u4(const float* w, int64_t n_elems, int32_t group, uint8_t* codes,
+                      uint16_t* pairs, void* stream);
+
+/* out [N, K] = the weight's values, m + s * c rounded once to fp32 and then
+ * to bf16 (_f16: fp16), nearest even.                                       */
+int qlora_dequantize_u4(const qlora_u4_weight* w, uint16_t* out, void* stream);
+int qlora_dequantize_u4_f16(const qlora_u4_weight* w, uint16_t* out, void* stream);
+
+/* y = x . W^T for few tokens: x [M, K] and y [M, N] bf16 (_f16: fp16), with
+ * rows ldx >= K and ldy >= N elements apart (x 16-byte aligned and ldx a
+ * multiple of 8, EALIGN; y needs the alignment of its type only).  The
+ * weight's values enter exactly (never rounded to 16 bits), sums are fp32
+ * and y is rounded once.  Any M, N >= 1; the kernel reads the weight once
+ * per 64 tokens, so it is meant for M up to about that.  M = 0 enqueues
+ * nothing.  No workspace; the same bits on every run.                       */
+int qlora_linear_u4_fwd(const qlora_u4_weight* w, const uint16_t* x, int64_t ldx, int64_t M,
+                        uint16_t* y, int64_t ldy, void* stream);
+int qlora_linear_u4_fwd_f16(const qlora_u4_weight* w, const uint16_t* x, int64_t ldx, int64_t M,
+                            uint16_t* y, int64_t ldy, void* stream);
+
+/* The paged cache: a pool of pages, each with page_size tokens of every KV
+ * head, keys and values in the 4-bit group format with one group per
+ * (token, head).  The pool's memory need not be initialised.               */
+typedef struct qlora_kv4_cache {
+  uint8_t*  k_codes;   /* [pages, kv_heads, page_size, head_dim/2] */
+  uint16_t* k_pairs;   /* [pages, kv_heads, page_size, 2]          */
+  uint8_t*  v_codes;
+  uint16_t* v_pairs;
+  int64_t   pages;     /* below 2^31 (ESHAPE)                      */
+  int32_t   page_size; /* a power of two, 16 .. 1024 (ENOTSUP)     */
+  int32_t   kv_heads;  /* up to 4096 (ESHAPE)                      */
+  int32_t   head_dim;  /* 64, 128 or 256 (ENOTSUP)                 */
+} qlora_kv4_cache;
+
+/* A ragged batch.  Sequence b has the rows cu_q[b] .. cu_q[b+1] - 1 of the
+ * call's row tensors (none, one at a decode step, many at a prefill); they
+ * are the last tokens of its seq_lens[b], so row i of n sits at position
+ * seq_lens[b] - n + i.  Position p lies in row p % page_size of page
+ * block_table[b][p / page_size].  The arrays are device memory that the
+ * host does not see; on the device,
+ *   - rows past `rows` and beyond `max_q` of a sequence are not worked on,
+ *     and rows behind cu_q[seqs] are left as they were;
+ *   - a position without a page (past the table, or an entry outside
+ *     0 .. pages - 1, such as -1 for a page given back) is a token that is
+ *     not there: not stored, not attended to, read as zeros;
+ *   - a page may belong to several sequences (a shared prefix), but no two
+ *     rows of one append may name the same token of the same page.          */
+typedef struct qlora_kv4_batch {
+  const int32_t* cu_q;        /* [seqs + 1], ascending from 0          */
+  const int32_t* seq_lens;    /* [seqs], with the rows of this call    */
+  const int32_t* block_table; /* [seqs, table_width]                   */
+  int64_t        rows;        /* rows of the row tensors, up to 2^30   */
+  int32_t        seqs;        /* up to 65535 (ESHAPE)                  */
+  int32_t        table_width; /* table_width * page_size up to 2^30    */
+  int32_t        max_q;       /* at least the most rows of a sequence  */
+} qlora_kv4_batch;
+
+/* Append the batch's keys and values to the cache, rotated by position.
+ *   k, v [rows, kv_heads, head_dim], q [rows, q_heads, head_dim] bf16
+ *     (_f16: fp16), element (t, h, d) at t * ts + h * hs + d (multiples of
+ *     8, EALIGN), so slices of one projection's output can be passed.
+ *   q_heads = 0: no queries (q and q_out may be NULL).
+ *   cos_sin [table_rows, rot] fp32: row p has the rot/2 cosines, then the
+ *     rot/2 sines of position p.  The first rot values of a head are
+ *     rotated in pairs: (i, i + rot/2), or neighbours (2i, 2i + 1) where
+ *     interleaved is nonzero; (a, b) -> (a cos - b sin, b cos + a sin).
+ *     rot is 0 (no rotation; cos_sin may be NULL) or a multiple of 8 up to
+ *     head_dim (ESHAPE).
+ *   q_out [rows, q_heads, head_dim], densely packed: the rotated queries,
+ *     rounded once.  Keys are encoded from the unrounded rotation.
+ * A row at a negative position, or past the cos_sin table, stores nothing
+ * and its q_out is NaN.  No workspace.                                      */
+int qlora_kv4_append(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, const uint16_t* k,
+                     int64_t k_ts, int64_t k_hs, const uint16_t* v, int64_t v_ts, int64_t v_hs,
+                     const uint16_t* q, int64_t q_ts, int64_t q_hs, int32_t q_heads,
+                     const float* cos_sin, int64_t table_rows, int32_t rot, int32_t interleaved,
+                     uint16_t* q_out, void* stream);
+int qlora_kv4_append_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch,
+                         const uint16_t* k, int64_t k_ts, int64_t k_hs, const uint16_t* v,
+                         int64_t v_ts, int64_t v_hs, const uint16_t* q, int64_t q_ts, int64_t q_hs,
+                         int32_t q_heads, const float* cos_sin, int64_t table_rows, int32_t rot,
+                         int32_t interleaved, uint16_t* q_out, void* stream);
+
+/* The values that the cache holds for the batch's rows (as the tokens
+ * qlora_kv4_append stored for the same batch, or any others: the rows say
+ * which), into k_out and v_out [rows, kv_heads, head_dim], densely packed.
+ * Tokens that are not there read as zeros.                                  */
+int qlora_kv4_read(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, uint16_t* k_out,
+                   uint16_t* v_out, void* stream);
+int qlora_kv4_read_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, uint16_t* k_out,
+                       uint16_t* v_out, void* stream);
+
+/* Attention of the batch's rows over the cache (after qlora_kv4_append):
+ *   out = softmax(scale q . k^T over the visible keys) . v
+ *   q [rows, q_heads, head_dim] with strides as above; q_heads a multiple
+ *     of kv_heads (ESHAPE), query head h reads KV head
+ *     h / (q_heads / kv_heads).
+ *   A row at position p sees the tokens 0 <= j < seq_lens[b] of its
+ *     sequence that have a page, with causal nonzero those with j <= p, with
+ *     window > 0 those with j > p - window.
+ *   max_len: at least the longest seq_lens (it sets how the keys are split
+ *     over the chip and the workspace; a sequence that is longer all the
+ *     same is attended in full, with larger shares).
+ *   out [rows, q_heads, head_dim], densely packed, rounded once from fp32;
+ *   lse [rows, q_heads] fp32 (or NULL): the logarithm of the sum of
+ *     exp(score).  A row that sees nothing gets zeros and -infinity.
+ *   What a hidden token's memory holds, NaN included, has no effect.
+ * scale must be finite (EINVAL).  workspace (256-byte aligned): at least
+ * qlora_kv4_attention_workspace_bytes(seqs, max_q, max_len, ...) bytes, or
+ * NULL where that is 0 (also its answer for an invalid shape); it is written
+ * before it is read.  Host-only; the same bits on every run of a shape.     */
+size_t qlora_kv4_attention_workspace_bytes(int64_t seqs, int64_t max_q, int64_t max_len,
+                                           int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                           int32_t window);
+int qlora_kv4_attention(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch,
+                        const uint16_t* q, int64_t q_ts, int64_t q_hs, int32_t q_heads,
+                        float scale, int32_t causal, int32_t window, int64_t max_len,
+                        uint16_t* out, float* lse, void* workspace, size_t ws_bytes,
+                        void* stream);
+int qlora_kv4_attention_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch,
+                            const uint16_t* q, int64_t q_ts, int64_t q_hs, int32_t q_heads,
+                            float scale, int32_t causal, int32_t window, int64_t max_len,
+                            uint16_t* out, float* lse, void* workspace, size_t ws_bytes,
+                            void* stream);
+
 /* Workspace bytes for op 0 (forward) or 1 (backward) of the NF4 layer,
  * op 2 (forward) or 3 (backward) of the bf16-weight layer, op 4 (forward)
  * or 5 (backward) of the NF4 layer with dropout, op 6 (forward) or 7

@@ -1,0 +1,238 @@
+"""Refusals of the 4-bit serving calls, without a GPU: every one comes from
+validation before any HIP call (the addresses are fake) or from the Python
+checks."""
+
+import ctypes
+import os
+
+import pytest
+
+import bit_quantized_lora_03_amd as q
+from bit_quantized_lora_03_amd import _lib
+
+pytestmark = pytest.mark.skipif(not os.path.exists(q.LIB_PATH), reason="libqlora.so not built")
+
+MB = 1 << 20
+OK, EINVAL, ESHAPE, EALIGN, ENOTSUP, EWORKSPACE = 0, -1, -2, -3, -4, -5
+
+
+def at(i):
+    return (i + 1) * 64 * MB
+
+
+def test_quantize_refusals():
+    f = q.lib().qlora_quantize_u4
+    w, c, p = at(0), at(1), at(2)
+    assert f(w, 0, 64, c, p, None) == OK                # nothing to do, nothing launched
+    assert f(None, 0, 64, None, None, None) == OK
+    assert f(w, -64, 64, c, p, None) == EINVAL
+    for g in (0, 16, 48, 256, -64):
+        assert f(w, 4096, g, c, p, None) == ENOTSUP
+    assert f(w, 4096 + 32, 64, c, p, None) == ESHAPE
+    for bad in ((None, c, p), (w, None, p), (w, c, None)):
+        assert f(bad[0], 4096, 64, bad[1], bad[2], None) == EINVAL
+    for bad in ((w + 4, c, p), (w, c + 8, p), (w, c, p + 4)):
+        assert f(bad[0], 4096, 64, bad[1], bad[2], None) == EALIGN
+    assert f(w, 4096, 64, w + 16, p, None) == EINVAL    # codes inside w
+    assert f(w, 4096, 64, c, c + 1024, None) == EINVAL  # pairs inside codes
+
+
+def weight(**kw):
+    d = dict(codes=at(0), pairs=at(1), N=128, K=256, group=64)
+    d.update(kw)
+    return ctypes.byref(_lib.U4Struct(d["codes"], d["pairs"], d["N"], d["K"], d["group"]))
+
+
+BAD_WEIGHTS = [
+    (dict(codes=None), EINVAL), (dict(pairs=None), EINVAL), (dict(N=0), EINVAL),
+    (dict(K=-64), EINVAL), (dict(group=16), ENOTSUP), (dict(group=0), ENOTSUP),
+    (dict(K=96), ESHAPE), (dict(N=1 << 30), ESHAPE), (dict(K=1 << 30), ESHAPE),
+    (dict(codes=at(0) + 4), EALIGN), (dict(pairs=at(1) + 2), EALIGN)]
+
+
+@pytest.mark.parametrize("kw,status", BAD_WEIGHTS)
+@pytest.mark.parametrize("tail", ["", "_f16"])
+def test_weight_refusals(kw, status, tail):
+    L = q.lib()
+    assert getattr(L, "qlora_dequantize_u4" + tail)(weight(**kw), at(5), None) == status
+    assert getattr(L, "qlora_linear_u4_fwd" + tail)(weight(**kw), at(3), 256, 4, at(5), 128,
+                                                    None) == status
+
+
+@pytest.mark.parametrize("tail", ["", "_f16"])
+def test_linear_and_dequantize_refusals(tail):
+    L = q.lib()
+    d = getattr(L, "qlora_dequantize_u4" + tail)
+    assert d(None, at(5), None) == EINVAL
+    assert d(weight(), None, None) == EINVAL
+    assert d(weight(), at(5) + 2, None) == EALIGN
+    assert d(weight(), at(0) + 512, None) == EINVAL
+    f = getattr(L, "qlora_linear_u4_fwd" + tail)
+    x, y = at(3), at(5)
+    assert f(weight(), x, 256, 0, y, 128, None) == OK
+    assert f(weight(), None, 256, 0, None, 128, None) == OK
+    assert f(None, x, 256, 4, y, 128, None) == EINVAL
+    assert f(weight(), None, 256, 4, y, 128, None) == EINVAL
+    assert f(weight(), x, 256, 4, None, 128, None) == EINVAL
+    assert f(weight(), x, 256, -1, y, 128, None) == EINVAL
+    assert f(weight(), x, 248, 4, y, 128, None) == EINVAL   # rows of x overlap
+    assert f(weight(), x, 256, 4, y, 127, None) == EINVAL   # rows of y overlap
+    assert f(weight(), x, 260, 4, y, 128, None) == EALIGN
+    assert f(weight(), x + 8, 256, 4, y, 128, None) == EALIGN
+    assert f(weight(), x, 256, 4, y + 1, 128, None) == EALIGN
+    assert f(weight(), x, 256, 1 << 40, y, 128, None) == ESHAPE
+    assert f(weight(), x, 256, 4, x + 512, 128, None) == EINVAL
+    assert f(weight(), x, 256, 4, at(1), 128, None) == EINVAL
+
+
+def cache(**kw):
+    d = dict(k_codes=at(0), k_pairs=at(1), v_codes=at(2), v_pairs=at(3), pages=4, page_size=16,
+             kv_heads=2, head_dim=64)
+    d.update(kw)
+    return ctypes.byref(_lib.Kv4CacheStruct(*[d[n] for n, _ in _lib.Kv4CacheStruct._fields_]))
+
+
+def batch(**kw):
+    d = dict(cu_q=at(4), seq_lens=at(5), block_table=at(6), rows=6, seqs=3, table_width=2, max_q=4)
+    d.update(kw)
+    return ctypes.byref(_lib.Kv4BatchStruct(*[d[n] for n, _ in _lib.Kv4BatchStruct._fields_]))
+
+
+BAD_CACHES = [
+    (dict(k_codes=None), EINVAL), (dict(k_pairs=None), EINVAL), (dict(v_codes=None), EINVAL),
+    (dict(v_pairs=None), EINVAL), (dict(pages=0), EINVAL), (dict(kv_heads=0), EINVAL),
+    (dict(head_dim=96), ENOTSUP), (dict(head_dim=0), ENOTSUP), (dict(page_size=8), ENOTSUP),
+    (dict(page_size=24), ENOTSUP), (dict(page_size=2048), ENOTSUP), (dict(page_size=0), ENOTSUP),
+    (dict(pages=1 << 31), ESHAPE), (dict(kv_heads=5000), ESHAPE),
+    (dict(k_codes=at(0) + 8), EALIGN), (dict(v_pairs=at(3) + 4), EALIGN)]
+BAD_BATCHES = [
+    (dict(cu_q=None), EINVAL), (dict(seq_lens=None), EINVAL), (dict(block_table=None), EINVAL),
+    (dict(rows=-1), EINVAL), (dict(seqs=-1), EINVAL), (dict(max_q=-1), EINVAL),
+    (dict(table_width=-1), EINVAL), (dict(seqs=65536), ESHAPE), (dict(rows=1 << 31), ESHAPE),
+    (dict(max_q=(1 << 30) + 1), ESHAPE), (dict(table_width=(1 << 26) + 1), ESHAPE),
+    (dict(cu_q=at(4) + 2), EALIGN), (dict(seq_lens=at(5) + 1), EALIGN),
+    (dict(block_table=at(6) + 2), EALIGN)]
+EMPTY = [dict(rows=0), dict(seqs=0), dict(max_q=0),
+         dict(rows=0, cu_q=None, seq_lens=None, block_table=None)]
+
+
+def call_append(c, b, tail="", **kw):
+    d = dict(k=at(10), kts=128, khs=64, v=at(11), vts=128, vhs=64, q=at(12), qts=256, qhs=64,
+             heads=4, table=at(13), rows=32, rot=64, inter=0, out=at(14))
+    d.update(kw)
+    return getattr(q.lib(), "qlora_kv4_append" + tail)(
+        c, b, d["k"], d["kts"], d["khs"], d["v"], d["vts"], d["vhs"], d["q"], d["qts"], d["qhs"],
+        d["heads"], d["table"], d["rows"], d["rot"], d["inter"], d["out"], None)
+
+
+def call_read(c, b, tail="", k=at(10), v=at(11)):
+    return getattr(q.lib(), "qlora_kv4_read" + tail)(c, b, k, v, None)
+
+
+def call_attention(c, b, tail="", **kw):
+    d = dict(q=at(12), qts=256, qhs=64, heads=4, scale=0.125, causal=1, window=0, max_len=32,
+             out=at(14), lse=at(15), ws=at(16), ws_bytes=64 * MB)
+    d.update(kw)
+    return getattr(q.lib(), "qlora_kv4_attention" + tail)(
+        c, b, d["q"], d["qts"], d["qhs"], d["heads"], d["scale"], d["causal"], d["window"],
+        d["max_len"], d["out"], d["lse"], d["ws"], d["ws_bytes"], None)
+
+
+CALLS = [call_append, call_read, call_attention]
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("tail", ["", "_f16"])
+def test_cache_and_batch_refusals(call, tail):
+    for kw, status in BAD_CACHES:
+        assert call(cache(**kw), batch(), tail) == status, kw
+    for kw, status in BAD_BATCHES:
+        assert call(cache(), batch(**kw), tail) == status, kw
+    assert call(None, batch(), tail) == EINVAL
+    assert call(cache(), None, tail) == EINVAL
+    for kw in EMPTY:
+        assert call(cache(), batch(**kw), tail) == OK, kw
+
+
+@pytest.mark.parametrize("tail", ["", "_f16"])
+def test_append_refusals(tail):
+    for kw, status in [
+            (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(q=None), EINVAL),
+            (dict(out=None), EINVAL), (dict(heads=-1), EINVAL), (dict(kts=-8), EINVAL),
+            (dict(rot=-8), EINVAL), (dict(rot=72), ESHAPE), (dict(rot=12), ESHAPE),
+            (dict(table=None), EINVAL), (dict(rows=0), EINVAL), (dict(rows=-1), EINVAL),
+            (dict(table=at(13) + 4), EALIGN), (dict(k=at(10) + 8), EALIGN),
+            (dict(kts=132), EALIGN), (dict(vhs=4), EALIGN), (dict(q=at(12) + 2), EALIGN),
+            (dict(out=at(14) + 8), EALIGN), (dict(kts=1 << 33), ESHAPE),
+            (dict(heads=70000), ESHAPE),
+            (dict(out=at(12)), EINVAL),                 # q_out over q
+            (dict(k=at(0)), EINVAL), (dict(out=at(2)), EINVAL), (dict(table=at(1)), EINVAL)]:
+        assert call_append(cache(), batch(), tail, **kw) == status, kw
+    assert call_append(cache(v_codes=at(0) + 64), batch(), tail) == EINVAL
+    assert call_append(cache(k_pairs=at(4)), batch(), tail) == EINVAL    # over cu_q
+
+
+@pytest.mark.parametrize("tail", ["", "_f16"])
+def test_read_refusals(tail):
+    for kw, status in [(dict(k=None), EINVAL), (dict(v=None), EINVAL),
+                       (dict(k=at(10) + 8), EALIGN), (dict(v=at(10)), EINVAL),
+                       (dict(k=at(0) + 16), EINVAL), (dict(v=at(6)), EINVAL)]:
+        assert call_read(cache(), batch(), tail, **kw) == status, kw
+
+
+@pytest.mark.parametrize("tail", ["", "_f16"])
+def test_attention_refusals(tail):
+    for kw, status in [
+            (dict(q=None), EINVAL), (dict(out=None), EINVAL), (dict(heads=0), EINVAL),
+            (dict(heads=3), ESHAPE), (dict(heads=1 << 17), ESHAPE), (dict(window=-1), EINVAL),
+            (dict(max_len=-1), EINVAL), (dict(max_len=(1 << 30) + 1), ESHAPE),
+            (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),
+            (dict(qts=100), EALIGN), (dict(q=at(12) + 4), EALIGN), (dict(out=at(14) + 8), EALIGN),
+            (dict(lse=at(15) + 2), EALIGN), (dict(out=at(12)), EINVAL),
+            (dict(lse=at(14) + 64), EINVAL), (dict(out=at(0)), EINVAL), (dict(lse=at(5)), EINVAL)]:
+        assert call_attention(cache(), batch(), tail, **kw) == status, kw
+    # a long axis needs room for partial results
+    long = dict(max_len=1 << 20)
+    b = batch(table_width=1 << 16)
+    need = q.kv4_attention_workspace_bytes(3, 4, 1 << 20, 4, 2, 64)
+    assert need > 0
+    assert call_attention(cache(), b, tail, ws=None, **long) == EWORKSPACE
+    assert call_attention(cache(), b, tail, ws_bytes=need - 1, **long) == EWORKSPACE
+    assert call_attention(cache(), b, tail, ws=at(16) + 128, ws_bytes=need, **long) == EALIGN
+    assert call_attention(cache(), b, tail, ws=at(14), ws_bytes=need, **long) == EINVAL
+    assert call_attention(cache(), b, tail, ws=at(12), ws_bytes=need, **long) == EINVAL
+
+
+def test_attention_workspace():
+    w = q.kv4_attention_workspace_bytes
+    assert w(64, 1, 100, 32, 8, 128) == 0               # one chunk: no partial results
+    assert w(1, 1, 1 << 17, 64, 8, 128) > 0
+    for bad in [(-1, 1, 8, 8, 8, 64), (1, -1, 8, 8, 8, 64), (1, 1, -1, 8, 8, 64),
+                (1, 1, 1 << 17, 8, 3, 64), (1, 1, 1 << 17, 8, 8, 80), (1, 1, 1 << 17, 0, 8, 64),
+                (70000, 1, 1 << 17, 8, 8, 64), (1, 1, 1 << 17, 8, 8, 64, -1)]:
+        assert w(*bad) == 0, bad
+    # a window bounds the keys of a row, so it bounds the workspace
+    assert w(1, 1, 1 << 20, 8, 8, 64, 1024) <= w(1, 1, 1 << 20, 8, 8, 64)
+
+
+def test_python_checks_refuse_before_the_library():
+    torch = pytest.importorskip("torch")
+    w = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        q.quantize_u4(w)                                # not on a GPU
+    with pytest.raises(ValueError):
+        q.U4Weight(torch.zeros(4, 32, dtype=torch.uint8),
+                   torch.zeros(4, 1, 2, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        q.Kv4Cache.empty(2, 16, 1, 64, device="cpu")
+    with pytest.raises(AttributeError):
+        q.no_such_call
+
+
+def test_importing_the_package_does_without_torch():
+    import subprocess
+    import sys
+    code = ("import sys, bit_quantized_lora_03_amd as q; assert 'torch' not in sys.modules; "
+            "q.linear_u4_fwd; assert 'torch' in sys.modules")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    assert subprocess.run([sys.executable, "-c", code], cwd=root).returncode == 0
