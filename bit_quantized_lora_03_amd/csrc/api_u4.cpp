@@ -13,6 +13,8 @@
 namespace {
 
 constexpr int64_t kMaxRows = int64_t{1} << 30;
+// The product's kernel reads 128 rows of codes and 64 of x with 32-bit offsets.
+constexpr int64_t kMaxK = int64_t{1} << 23;
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -51,7 +53,7 @@ int check_u4(const qlora_u4_weight* w) {
   if (!w || !w->codes || !w->pairs) return QLORA_EINVAL;
   if (w->N <= 0 || w->K <= 0) return QLORA_EINVAL;
   if (!group_ok(w->group)) return QLORA_ENOTSUP;
-  if (w->K % w->group || w->K >= kMaxRows || w->N >= kMaxRows) return QLORA_ESHAPE;
+  if (w->K % w->group || w->K > kMaxK || w->N >= kMaxRows) return QLORA_ESHAPE;
   if (!aligned(w->codes, 16) || !aligned(w->pairs, 16)) return QLORA_EALIGN;
   return QLORA_OK;
 }
@@ -81,7 +83,7 @@ int linear(const qlora_u4_weight* w, const uint16_t* x, int64_t ldx, int64_t M, 
     if (M < 0) return QLORA_EINVAL;
     if (M == 0) return QLORA_OK;
     if (!x || !y || ldx < w->K || ldy < w->N) return QLORA_EINVAL;
-    if (M > 65535 * 16 || ldx >= kMaxGrid || ldy >= kMaxGrid) return QLORA_ESHAPE;
+    if (M > 65535 * 16 || ldx > kMaxK || ldy >= kMaxGrid) return QLORA_ESHAPE;
     if (!aligned(x, 16) || ldx % 8 || !aligned(y, 2)) return QLORA_EALIGN;
     const size_t n = (size_t)w->N * w->K;
     if (clash<1, 3>({{y, ((size_t)(M - 1) * ldy + w->N) * 2}},

@@ -70,6 +70,15 @@ __device__ __forceinline__ uint32_t u4_code(const U4Coder& u, double v, float t)
 // 7-bit mantissa ends at the code with OFF = 128, rounds its operands far
 // above that; fp16 shifts the code to the mantissa's top, where OFF is 16.
 // The pairs of a word are (element j, element j + 4), j = 0..3.
+// (x & mask) | bits.  With both constant the compiler takes two instructions;
+// a constant whose origin it does not see sits in a register and takes one
+// (v_and_or_b32).  The empty statement is no instruction: one written out in
+// assembly would not be seen as a vector instruction whose result a following
+// MFMA has to wait for.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  asm("" : "+v"(bits));
+  return (x & mask) | bits;
+}
 template <class DT>
 struct U4Mfma;
 template <>
@@ -77,7 +86,7 @@ struct U4Mfma<Bf16T> {
   static constexpr float kOff = 128.0f;
   static constexpr uint32_t kOne = 0x3F803F80u;  // two ones
   static __device__ __forceinline__ uint32_t pair(uint32_t w, int j) {
-    return ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+    return and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u);
   }
 };
 template <>
@@ -86,7 +95,7 @@ struct U4Mfma<F16T> {
   static constexpr uint32_t kOne = 0x3C003C00u;
   static __device__ __forceinline__ uint32_t pair(uint32_t w, int j) {
     const int sh = 6 - 4 * j;
-    return ((sh > 0 ? w << sh : w >> -sh) & 0x03C003C0u) | 0x4C004C00u;
+    return and_or(sh > 0 ? w << sh : w >> -sh, 0x03C003C0u, 0x4C004C00u);
   }
 };
 // The 8 codes of a word as MFMA operand, in the order 0 4 1 5 2 6 3 7.

@@ -394,7 +394,7 @@ typedef struct qlora_u4_weight {
   const uint8_t*  codes;  /* [N, K/2]            */
   const uint16_t* pairs;  /* [N, K/group, 2]     */
   int64_t         N;      /* 1 .. 2^30 - 1       */
-  int64_t         K;      /* a multiple of group, below 2^30 (ESHAPE) */
+  int64_t         K;      /* a multiple of group, up to 2^23 (ESHAPE) */
   int32_t         group;  /* 32, 64 or 128 (ENOTSUP)                  */
 } qlora_u4_weight;
 
@@ -411,7 +411,8 @@ int qlora_dequantize_u4_f16(const qlora_u4_weight* w, uint16_t* out, void* strea
 
 /* y = x . W^T for few tokens: x [M, K] and y [M, N] bf16 (_f16: fp16), with
  * rows ldx >= K and ldy >= N elements apart (x 16-byte aligned and ldx a
- * multiple of 8, EALIGN; y needs the alignment of its type only).  The
+ * multiple of 8, EALIGN, up to 2^23, ESHAPE; y needs the alignment of its
+ * type only).  The
  * weight's values enter exactly (never rounded to 16 bits), sums are fp32
  * and y is rounded once.  Any M, N >= 1; the kernel reads the weight once
  * per 64 tokens, so it is meant for M up to about that.  M = 0 enqueues
