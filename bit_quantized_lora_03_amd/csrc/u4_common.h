@@ -66,9 +66,10 @@ __device__ __forceinline__ uint32_t u4_code(const U4Coder& u, double v, float t)
 // Products read the codes as 16-bit floats OFF + c, formed by putting the
 // code into the mantissa of a constant: two codes per v_and_or_b32 and no
 // conversion.  The offset leaves through sum(x (OFF + c)) - OFF sum(x),
-// which costs bits of the fp32 sum (7 at OFF = 128, 4 at 16): bf16, whose
-// 7-bit mantissa ends at the code with OFF = 128, rounds its operands far
-// above that; fp16 shifts the code to the mantissa's top, where OFF is 16.
+// which costs bits of the fp32 sum: 7 at OFF = 128, where bf16's mantissa
+// ends at the code's last bit, 4 at OFF = 16, with the code at the
+// mantissa's top and one more shift for 8 codes.  Results that are rounded
+// to bf16 take 128; fp16 ones, and scores, which become exponents, 16.
 // The pairs of a word are (element j, element j + 4), j = 0..3.
 // (x & mask) | bits.  With both constant the compiler takes two instructions;
 // a constant whose origin it does not see sits in a register and takes one
@@ -79,30 +80,37 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
   asm("" : "+v"(bits));
   return (x & mask) | bits;
 }
+template <uint32_t BITS, int SHIFT>
+struct U4Bits {  // the code SHIFT bits up in the 16-bit constant BITS
+  static __device__ __forceinline__ uint32_t pair(uint32_t w, int j) {
+    const int sh = SHIFT - 4 * j;
+    return and_or(sh > 0 ? w << sh : w >> -sh, 0x000F000Fu << SHIFT, BITS << 16 | BITS);
+  }
+};
 template <class DT>
-struct U4Mfma;
+struct U4Mfma;  // products whose sums are rounded to DT
 template <>
-struct U4Mfma<Bf16T> {
+struct U4Mfma<Bf16T> : U4Bits<0x4300, 0> {
   static constexpr float kOff = 128.0f;
   static constexpr uint32_t kOne = 0x3F803F80u;  // two ones
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, int j) {
-    return and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u);
-  }
 };
 template <>
-struct U4Mfma<F16T> {
+struct U4Mfma<F16T> : U4Bits<0x4C00, 6> {
   static constexpr float kOff = 16.0f;
   static constexpr uint32_t kOne = 0x3C003C00u;
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, int j) {
-    const int sh = 6 - 4 * j;
-    return and_or(sh > 0 ? w << sh : w >> -sh, 0x03C003C0u, 0x4C004C00u);
-  }
 };
-// The 8 codes of a word as MFMA operand, in the order 0 4 1 5 2 6 3 7.
 template <class DT>
+struct U4Score;  // products with an operand in DT whose sums are scores
+template <>
+struct U4Score<Bf16T> : U4Bits<0x4180, 3> {
+  static constexpr float kOff = 16.0f;
+};
+template <>
+struct U4Score<F16T> : U4Mfma<F16T> {};
+// The 8 codes of a word as MFMA operand, in the order 0 4 1 5 2 6 3 7.
+template <class OP>
 __device__ __forceinline__ u32x4_t u4_expand8(uint32_t w) {
-  return u32x4_t{U4Mfma<DT>::pair(w, 0), U4Mfma<DT>::pair(w, 1), U4Mfma<DT>::pair(w, 2),
-                 U4Mfma<DT>::pair(w, 3)};
+  return u32x4_t{OP::pair(w, 0), OP::pair(w, 1), OP::pair(w, 2), OP::pair(w, 3)};
 }
 // Eight 16-bit values in the same order.
 __device__ __forceinline__ u32x4_t u4_order8(u32x4_t v) {

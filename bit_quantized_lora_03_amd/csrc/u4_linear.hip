@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * W) void linear_u4_kernel(
     for (int g = 0; g < S::kPairs; ++g)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const u32x4_t b = u4_expand8<DT>(cw[g][c]);
+        const u32x4_t b = u4_expand8<U4Mfma<DT>>(cw[g][c]);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           d[g][t] = DT::mfma16(xo[g * C + c][t], b, c ? d[g][t] : f32x4_t{0, 0, 0, 0});
