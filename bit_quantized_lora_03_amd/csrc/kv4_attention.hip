@@ -70,56 +70,84 @@ __device__ __forceinline__ Span kv4_span(const Kv4Seq& sq, const Kv4AttnArg& a, 
   return s;
 }
 
+// A step's codes and pairs of keys and values, in the lane's places.
 template <int D>
 struct StepData {
-  static constexpr int KW = D / 32;             // words of key codes per half
+  static constexpr int KW = D / 32;                 // words of key codes per half
   static constexpr int VW = D == 64 ? 1 : D / 128;  // words of value codes per key
   uint32_t k[2][KW];
   uint32_t v[2][4][VW];
   u32x4_t kp[2], vp[2];
+};
+// Where the two halves of a step lie (the same for the wave).
+struct StepAt {
+  int64_t slot[2];
   bool ok[2];
 };
+// Lane offsets of a step's loads.
+struct LaneOffsets {
+  uint32_t k, v, p;
+};
 
-template <int D>
-__device__ __forceinline__ void load_step(StepData<D>& s, const Kv4CacheArg& c,
-                                          const int32_t* table, int width, int head, int t,
-                                          int hi, int lr, int lg) {
+__device__ __forceinline__ StepAt locate(const Kv4CacheArg& c, const int32_t* table, int width,
+                                         int head, int t, int hi) {
+  StepAt a;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int th = t + 16 * h, e = th >> c.page_log2;
     int page = th < hi && e < width ? table[e] : -1;
-    s.ok[h] = page >= 0 && page < c.pages;
-    page = s.ok[h] ? page : 0;
-    const int64_t slot =
+    a.ok[h] = page >= 0 && page < c.pages;
+    page = a.ok[h] ? page : 0;
+    a.slot[h] =
         (((int64_t)page * c.kv_heads + head) << c.page_log2) + (th & ((1 << c.page_log2) - 1));
-    const uint8_t* kc = c.k_codes + slot * (D / 2) + lr * (D / 2) + lg * (D / 8);
+  }
+  return a;
+}
+template <class T>
+__device__ __forceinline__ T load_at(const void* base, uint32_t off) {
+  return *reinterpret_cast<const T*>(static_cast<const uint8_t*>(base) + off);
+}
+template <int D>
+__device__ __forceinline__ void load_keys(StepData<D>& s, const Kv4CacheArg& c, const StepAt& a,
+                                          const LaneOffsets& lo) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint8_t* kc = c.k_codes + a.slot[h] * (D / 2);
     if constexpr (D == 64) {
-      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(kc);
+      const u32x2_t w = load_at<u32x2_t>(kc, lo.k);
       s.k[h][0] = w[0];
       s.k[h][1] = w[1];
     } else {
 #pragma unroll
       for (int q = 0; q < D / 128; ++q) {
-        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(kc + 16 * q);
+        const u32x4_t w = load_at<u32x4_t>(kc, lo.k + 16u * q);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s.k[h][4 * q + i] = w[i];
       }
     }
-    s.kp[h] = *reinterpret_cast<const u32x4_t*>(c.k_pairs + slot + 4 * lg);
-    const uint8_t* vc = c.v_codes + (slot + 4 * lg) * (D / 2) + lr * (D / 32);
+    s.kp[h] = load_at<u32x4_t>(c.k_pairs + a.slot[h], lo.p);
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_values(StepData<D>& s, const Kv4CacheArg& c, const StepAt& a,
+                                            const LaneOffsets& lo) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint8_t* vc = c.v_codes + a.slot[h] * (D / 2);
+    s.vp[h] = load_at<u32x4_t>(c.v_pairs + a.slot[h], lo.p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const uint32_t off = lo.v + (uint32_t)(i * (D / 2));
       if constexpr (D == 64) {
-        s.v[h][i][0] = *reinterpret_cast<const uint16_t*>(vc + i * (D / 2));
+        s.v[h][i][0] = load_at<uint16_t>(vc, off);
       } else if constexpr (D == 128) {
-        s.v[h][i][0] = *reinterpret_cast<const uint32_t*>(vc + i * (D / 2));
+        s.v[h][i][0] = load_at<uint32_t>(vc, off);
       } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(vc + i * (D / 2));
+        const u32x2_t w = load_at<u32x2_t>(vc, off);
         s.v[h][i][0] = w[0];
         s.v[h][i][1] = w[1];
       }
     }
-    s.vp[h] = *reinterpret_cast<const u32x4_t*>(c.v_pairs + slot + 4 * lg);
   }
 }
 
@@ -134,7 +162,7 @@ __device__ __forceinline__ float column_max(float v) {
 }
 
 template <class DT, int D, int NT>
-__global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_kernel(
     Kv4CacheArg c, Kv4BatchArg bt, Kv4AttnArg a, int chunk, int splits, int tiles,
     float* __restrict__ part_o, float* __restrict__ part_ml) {
   constexpr int KC = D / 32;  // score products per half
@@ -164,6 +192,9 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
   float qsum[NT];
   int row_lo[NT], row_n[NT];
   const u32x4_t ones = {U4Mfma<DT>::kOne, U4Mfma<DT>::kOne, U4Mfma<DT>::kOne, U4Mfma<DT>::kOne};
+  // a negative scale turns the queries' signs, so that the largest product is
+  // the largest score
+  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = min(r0 + 16 * n + lr, rows - 1), i = r / group;
@@ -172,7 +203,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
     f32x4_t qs = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
-      q[n][k] = u4_order8(*reinterpret_cast<const u32x4_t*>(p + lg * (D / 4) + 8 * k));
+      q[n][k] = u4_order8(*reinterpret_cast<const u32x4_t*>(p + lg * (D / 4) + 8 * k)) ^ flip;
       qs = DT::mfma16(ones, q[n][k], qs);
     }
     qsum[n] = qs[0];
@@ -193,17 +224,22 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
 #pragma unroll
     for (int j = 0; j < VC; ++j) o[n][j] = f32x4_t{0, 0, 0, 0};
     po[n] = f32x4_t{0, 0, 0, 0};
-    m[n] = -INFINITY;  // running maximum (log2 units)
-    mu[n] = 0.0f;      // the same, 0 while it is -inf
+    m[n] = -INFINITY;  // running maximum of the products q.k
+    mu[n] = 0.0f;      // the same in log2 units, 0 while it is -inf
     l[n] = cs[n] = 0.0f;
   }
-  const float c1 = a.scale * kLog2e;
+  const float c1 = fabsf(a.scale) * kLog2e;
+  const float slack = fminf(kSlack / c1, 3e38f);  // any product is within it where the scale is 0
+  const LaneOffsets lane_at = {(uint32_t)(lr * (D / 2) + lg * (D / 8)),
+                               (uint32_t)(4 * lg * (D / 2) + lr * (D / 32)), 16u * lg};
   const u32x4_t onesv = {U4Mfma<Bf16T>::kOne, U4Mfma<Bf16T>::kOne, U4Mfma<Bf16T>::kOne,
                          U4Mfma<Bf16T>::kOne};
   const int32_t* table = bt.block_table + (int64_t)b * bt.table_width;
 
-  auto step = [&](const StepData<D>& s, int t) {
-    const bool masked = !(s.ok[0] && s.ok[1]) || t < all_lo || t + kStep > all_hi;
+  // one step; the next one's keys are asked for once these are used, and its
+  // values likewise, so one set of registers serves both
+  auto step = [&](StepData<D>& s, const StepAt& at, const StepAt& next, bool more, int t) {
+    const bool masked = !(at.ok[0] && at.ok[1]) || t < all_lo || t + kStep > all_hi;
     // scores
     f32x4_t z[NT][2];
 #pragma unroll
@@ -219,11 +255,12 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float ks = u4_s(s.kp[h][i]);
-        const float km = fmaf(-kOffK, ks, u4_m(s.kp[h][i])) * c1;
+        const float km = fmaf(-kOffK, ks, u4_m(s.kp[h][i]));
 #pragma unroll
-        for (int n = 0; n < NT; ++n) z[n][h][i] = fmaf(ks * c1, z[n][h][i], km * qsum[n]);
+        for (int n = 0; n < NT; ++n) z[n][h][i] = fmaf(ks, z[n][h][i], km * qsum[n]);
       }
     }
+    if (more) load_keys<D>(s, c, next, lane_at);
     u32x4_t pb[NT], pl[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -234,7 +271,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const bool v = s.ok[h] &&
+            const bool v = at.ok[h] &&
                            (uint32_t)(t + 16 * h + 4 * lg + i - row_lo[n]) < (uint32_t)row_n[n];
             z[n][h][i] = v ? z[n][h][i] : -INFINITY;
             vis |= (v ? 1u : 0u) << (4 * h + i);
@@ -242,11 +279,12 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
       }
       float top = fmaxf(fmaxf(fmaxf(z[n][0][0], z[n][0][1]), fmaxf(z[n][0][2], z[n][0][3])),
                         fmaxf(fmaxf(z[n][1][0], z[n][1][1]), fmaxf(z[n][1][2], z[n][1][3])));
-      if (__any(top > m[n] + kSlack)) {
+      if (__any(top > m[n] + slack)) {
         top = fmaxf(column_max(top), m[n]);
-        const float f = exp2f(m[n] - (top == -INFINITY ? 0.0f : top));
+        const float was = m[n] == -INFINITY ? -INFINITY : mu[n];
         m[n] = top;
-        mu[n] = top == -INFINITY ? 0.0f : top;
+        mu[n] = top == -INFINITY ? 0.0f : top * c1;
+        const float f = exp2f(was - mu[n]);
 #pragma unroll
         for (int j = 0; j < VC; ++j)
 #pragma unroll
@@ -261,14 +299,15 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float p = __builtin_amdgcn_exp2f(z[n][h][i] - mu[n]);
-          l[n] += p;
+          float p = __builtin_amdgcn_exp2f(fmaf(z[n][h][i], c1, -mu[n]));
           float vs = u4_s(s.vp[h][i]), vm = fmaf(kMid, vs, u4_m(s.vp[h][i]));
           if (masked) {  // whatever a hidden key's pair holds is not read
             const bool v = vis >> (4 * h + i) & 1;
             vs = v ? vs : 0.0f;
             vm = v ? vm : 0.0f;
+            p = v ? p : 0.0f;  // -inf times a scale of 0
           }
+          l[n] += p;
           ps[h][i] = p * vs;
           cs[n] = fmaf(p, vm, cs[n]);
         }
@@ -304,19 +343,28 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
         }
       }
     }
+    if (more) load_values<D>(s, c, next, lane_at);
   };
 
-  StepData<D> cur, nxt;
+  constexpr int kStride = kStep * kWaves;
   int t = t0 + kStep * wave;
-  if (t < t1) load_step<D>(cur, c, table, bt.table_width, head, t, sp.hi, lr, lg);
-  for (; t < t1; t += kStep * kWaves) {
-    const int tn = t + kStep * kWaves;
-    if (tn < t1) load_step<D>(nxt, c, table, bt.table_width, head, tn, sp.hi, lr, lg);
-    step(cur, t);
-    cur = nxt;
+  if (t < t1) {
+    auto find = [&](int at) { return locate(c, table, bt.table_width, head, at, sp.hi); };
+    StepData<D> s;
+    StepAt at = find(t);
+    load_keys<D>(s, c, at, lane_at);
+    load_values<D>(s, c, at, lane_at);
+    for (; t < t1; t += kStride) {
+      const bool more = t + kStride < t1;
+      const StepAt next = find(more ? t + kStride : t);
+      step(s, at, next, more, t);
+      at = next;
+    }
   }
 
-  // join the four waves
+  // join the four waves, their maxima in log2 units
+#pragma unroll
+  for (int n = 0; n < NT; ++n) m[n] = m[n] == -INFINITY ? m[n] : mu[n];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     l[n] = column_sum(l[n]);
@@ -385,48 +433,61 @@ __global__ __launch_bounds__(64 * kWaves) void kv4_attention_kernel(
   }
 }
 
-// Joins the chunks of one query row: a block is D / 4 lanes times kJoin
-// shares of the chunks.
+// Joins the chunks of the query rows: a row is D / 4 lanes times J shares of
+// its chunks, 256 / (D / 4) / J rows a block.
 constexpr int kJoinThreads = 256;
-template <class DT, int D>
+template <class DT, int D, int J>
 __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(
     Kv4CacheArg c, Kv4BatchArg bt, Kv4AttnArg a, int tile_rows, int chunk, int splits, int tiles,
     const float* __restrict__ part_o, const float* __restrict__ part_ml) {
-  constexpr int LPV = D / 4, J = kJoinThreads / LPV;
-  __shared__ f32x4_t o_lds[J][LPV];
-  __shared__ float l_lds[J];
+  constexpr int LPV = D / 4, RPB = kJoinThreads / LPV / J;
+  __shared__ f32x4_t o_lds[RPB][J][LPV];
+  __shared__ float l_lds[RPB][J], m_lds[RPB][J];
   const int b = blockIdx.z, head = blockIdx.y;
-  const int tile = blockIdx.x / tile_rows, rr = blockIdx.x - tile * tile_rows;
   const int group = a.q_heads / c.kv_heads;
   const Kv4Seq sq = kv4_seq(bt, b);
-  const int r0 = tile * tile_rows, r = r0 + rr, rows = (int)(sq.n * group);
-  if (r >= rows) return;
-  const Span sp = kv4_span(sq, a, group, r0, tile_rows, chunk, splits);
-  if (sp.n <= 1) return;  // already written
-  const int64_t base =
-      (((int64_t)b * c.kv_heads + head) * tiles + tile) * splits * tile_rows + rr;
-  float top = -INFINITY;
-  for (int s = threadIdx.x & 63; s < sp.n; s += 64)
-    top = fmaxf(top, part_ml[2 * (base + (int64_t)s * tile_rows)]);
-#pragma unroll
-  for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-  const int j = threadIdx.x / LPV, d = threadIdx.x % LPV;
+  const int d = threadIdx.x % LPV, j = threadIdx.x / LPV % J, rb = threadIdx.x / LPV / J;
+  const int r = blockIdx.x * RPB + rb, rows = (int)(sq.n * group);
+  const int tile = r / tile_rows, rr = r - tile * tile_rows;
   f32x4_t v = {0, 0, 0, 0};
-  float sum = 0.0f;
-  for (int s = j; s < sp.n; s += J) {
-    const int64_t at = base + (int64_t)s * tile_rows;
-    const float ms = part_ml[2 * at], f = ms == -INFINITY ? 0.0f : exp2f(ms - top);
-    sum = fmaf(part_ml[2 * at + 1], f, sum);
-    v += *reinterpret_cast<const f32x4_t*>(part_o + at * D + 4 * d) * f;
+  float sum = 0.0f, top = -INFINITY;  // of this share
+  bool mine = r < rows;
+  if (mine) {
+    const Span sp = kv4_span(sq, a, group, tile * tile_rows, tile_rows, chunk, splits);
+    mine = sp.n > 1;  // with one chunk it is already written
+    if (mine) {
+      const int64_t base =
+          (((int64_t)b * c.kv_heads + head) * tiles + tile) * splits * tile_rows + rr;
+      for (int s = j; s < sp.n; s += J)
+        top = fmaxf(top, part_ml[2 * (base + (int64_t)s * tile_rows)]);
+      for (int s = j; s < sp.n; s += J) {
+        const int64_t at = base + (int64_t)s * tile_rows;
+        const float ms = part_ml[2 * at], f = ms == -INFINITY ? 0.0f : exp2f(ms - top);
+        sum = fmaf(part_ml[2 * at + 1], f, sum);
+        v += *reinterpret_cast<const f32x4_t*>(part_o + at * D + 4 * d) * f;
+      }
+    }
   }
-  o_lds[j][d] = v;
-  if (d == 0) l_lds[j] = sum;
-  __syncthreads();
-  if (j > 0) return;
-  for (int w = 1; w < J; ++w) {
-    v += o_lds[w][d];
-    sum += l_lds[w];
+  if constexpr (J > 1) {
+    o_lds[rb][j][d] = v;
+    if (d == 0) {
+      l_lds[rb][j] = sum;
+      m_lds[rb][j] = top;
+    }
+    __syncthreads();
+    if (j > 0) return;
+#pragma unroll
+    for (int w = 1; w < J; ++w) top = fmaxf(top, m_lds[rb][w]);
+    v = f32x4_t{0, 0, 0, 0};
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < J; ++w) {
+      const float mw = m_lds[rb][w], f = mw == -INFINITY ? 0.0f : exp2f(mw - top);
+      v += o_lds[rb][w][d] * f;
+      sum = fmaf(l_lds[rb][w], f, sum);
+    }
   }
+  if (!mine) return;
   const int i = r / group, hq = head * group + r - i * group;
   const int64_t at = (sq.row0 + i) * a.q_heads + hq;
   const bool none = top == -INFINITY && sum == 0.0f;
@@ -445,9 +506,17 @@ void go(const Kv4CacheArg& c, const Kv4BatchArg& b, const Kv4AttnArg& a, const K
   kv4_attention_kernel<DT, D, 1>
       <<<grid, 64 * kWaves, 0, s>>>(c, b, a, p.chunk, p.splits, p.tiles, ws, ml);
   if (p.splits > 1) {
-    const dim3 jgrid((unsigned)(p.tile * p.tiles), (unsigned)c.kv_heads, (unsigned)b.seqs);
-    kv4_join_kernel<DT, D><<<jgrid, kJoinThreads, 0, s>>>(c, b, a, p.tile, p.chunk, p.splits,
-                                                          p.tiles, ws, ml);
+    const int64_t rows = (int64_t)b.max_q * (a.q_heads / c.kv_heads);
+    auto join = [&](auto jc) {
+      constexpr int J = decltype(jc)::value, RPB = kJoinThreads / (D / 4) / J;
+      const dim3 jgrid((unsigned)((rows + RPB - 1) / RPB), (unsigned)c.kv_heads, (unsigned)b.seqs);
+      kv4_join_kernel<DT, D, J><<<jgrid, kJoinThreads, 0, s>>>(c, b, a, p.tile, p.chunk, p.splits,
+                                                               p.tiles, ws, ml);
+    };
+    if (p.splits <= 8)
+      join(std::integral_constant<int, 1>{});
+    else
+      join(std::integral_constant<int, kJoinThreads / (D / 4)>{});
   }
 }
 
@@ -462,7 +531,7 @@ Kv4AttnPlan kv4_attn_plan(int64_t seqs, int64_t max_q, int64_t max_len, int q_he
   int64_t keys = max_len;
   // a tile's window starts up to 31 keys early
   if (window > 0 && window + max_q + kStep < keys) keys = window + max_q + kStep;
-  const int64_t want = 1536, base = seqs * kv_heads * p.tiles;
+  const int64_t want = 4096, base = seqs * kv_heads * p.tiles;
   const int64_t per = kStep * kWaves;
   int64_t chunk = (keys * base + want - 1) / want;
   chunk = (chunk + per - 1) / per * per;
