@@ -70,83 +70,92 @@ __device__ __forceinline__ Span kv4_span(const Kv4Seq& sq, const Kv4AttnArg& a, 
   return s;
 }
 
-// A step's codes and pairs of keys and values, in the lane's places.
+// A wave's LDS: a ring of stages, each with one step's keys, values (32 rows
+// of D / 2 bytes) and their pairs (16 words each: keys of both halves, values
+// of both).  The 16-byte pieces of a row are exchanged so that neither the
+// 16 rows of a key operand nor the 4 keys of a value read share banks.
 template <int D>
-struct StepData {
-  static constexpr int KW = D / 32;                 // words of key codes per half
-  static constexpr int VW = D == 64 ? 1 : D / 128;  // words of value codes per key
-  uint32_t k[2][KW];
-  uint32_t v[2][4][VW];
-  u32x4_t kp[2], vp[2];
+struct Ring {
+  static constexpr int kCodes = 16 * D, kStage = 2 * kCodes + 256;
+  static constexpr int kPieces = D / 32, kRowsPerBanks = 512 / D;
+  static constexpr int kHalfLoads = D == 256 ? 2 : 1;  // DMA instructions for a half's keys
+  static constexpr int kAll = 4 * kHalfLoads + 4;      // ... and for a step
+  // Two stages in flight beside the one in use; at D = 256 one, so that two
+  // blocks fit a CU.
+  static constexpr int kStages = D == 256 ? 2 : 3;
+  static __device__ __forceinline__ uint32_t place(uint32_t row, uint32_t piece) {
+    return row * (D / 2) + ((piece ^ (row / kRowsPerBanks)) & (kPieces - 1)) * 16;
+  }
 };
-// Where the two halves of a step lie (the same for the wave).
-struct StepAt {
-  int64_t slot[2];
-  bool ok[2];
+// The pages of a step's two halves as the block table has them (-1: none).
+// The table is read through the constant address space: by scalar loads.
+typedef const __attribute__((address_space(4))) int32_t* TablePtr;
+struct StepPages {
+  int page[2];
 };
-// Lane offsets of a step's loads.
-struct LaneOffsets {
-  uint32_t k, v, p;
-};
-
-__device__ __forceinline__ StepAt locate(const Kv4CacheArg& c, const int32_t* table, int width,
-                                         int head, int t, int hi) {
-  StepAt a;
+__device__ __forceinline__ StepPages look_up(const Kv4CacheArg& c, TablePtr table, int width,
+                                             int t, int hi) {
+  StepPages p;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int th = t + 16 * h, e = th >> c.page_log2;
-    int page = th < hi && e < width ? table[e] : -1;
-    a.ok[h] = page >= 0 && page < c.pages;
-    page = a.ok[h] ? page : 0;
-    a.slot[h] =
-        (((int64_t)page * c.kv_heads + head) << c.page_log2) + (th & ((1 << c.page_log2) - 1));
+    p.page[h] = th < hi && e < width ? table[e] : -1;
   }
-  return a;
+  return p;
 }
-template <class T>
-__device__ __forceinline__ T load_at(const void* base, uint32_t off) {
-  return *reinterpret_cast<const T*>(static_cast<const uint8_t*>(base) + off);
+// Which halves have a page, as bits.
+__device__ __forceinline__ uint32_t there(const Kv4CacheArg& c, const StepPages& p) {
+  const uint32_t pages = (uint32_t)c.pages;
+  return ((uint32_t)p.page[0] < pages ? 1u : 0u) | ((uint32_t)p.page[1] < pages ? 2u : 0u);
 }
+
+// 16 (4) bytes a lane from a buffer straight to LDS, lane after lane.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t from, uint32_t off, uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16,
+                                           off, 0, 0, 0);
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t from, uint32_t off, uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 4,
+                                           off, 0, 0, 0);
+}
+// s_waitcnt immediate: at most `vm` vector-memory operations outstanding.
+constexpr int wait_vm(int vm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | (15 << 8); }
+
+// One step's keys, values and pairs into a stage, straight to LDS: lane l of
+// a load brings its 16 bytes l (4 of the pairs).  Each half's 16 rows are a
+// buffer of their own.  A half without a page brings page 0's.
 template <int D>
-__device__ __forceinline__ void load_keys(StepData<D>& s, const Kv4CacheArg& c, const StepAt& a,
-                                          const LaneOffsets& lo) {
+__device__ __forceinline__ void fetch(const Kv4CacheArg& c, const StepPages& p, uint32_t have,
+                                      int head, int t, uint8_t* to, int lane) {
+  using R = Ring<D>;
+  // the lane's piece of a KiB (or of the half's 512 bytes at D = 64)
+  uint32_t off[R::kHalfLoads];
+#pragma unroll
+  for (int i = 0; i < R::kHalfLoads; ++i) {
+    const uint32_t row = (1024u * i + 16u * lane) / (D / 2);
+    const uint32_t piece = (lane ^ row / R::kRowsPerBanks) & (R::kPieces - 1);
+    off[i] = row * (D / 2) + piece * 16;
+  }
+  constexpr int kHalf = 8 * D;  // bytes of a half's codes
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint8_t* kc = c.k_codes + a.slot[h] * (D / 2);
-    if constexpr (D == 64) {
-      const u32x2_t w = load_at<u32x2_t>(kc, lo.k);
-      s.k[h][0] = w[0];
-      s.k[h][1] = w[1];
-    } else {
+    const int page = have >> h & 1 ? p.page[h] : 0;
+    const int64_t slot = (((int64_t)page * c.kv_heads + head) << c.page_log2) +
+                         ((t + 16 * h) & ((1 << c.page_log2) - 1));
+    const __amdgpu_buffer_rsrc_t kc = make_rsrc(c.k_codes + slot * (D / 2), kHalf);
+    const __amdgpu_buffer_rsrc_t vc = make_rsrc(c.v_codes + slot * (D / 2), kHalf);
+    const __amdgpu_buffer_rsrc_t kp = make_rsrc(c.k_pairs + slot, 64);
+    const __amdgpu_buffer_rsrc_t vp = make_rsrc(c.v_pairs + slot, 64);
+    if (D > 64 || lane < 32) {
 #pragma unroll
-      for (int q = 0; q < D / 128; ++q) {
-        const u32x4_t w = load_at<u32x4_t>(kc, lo.k + 16u * q);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s.k[h][4 * q + i] = w[i];
+      for (int i = 0; i < R::kHalfLoads; ++i) {
+        dma16(kc, off[i], to + h * kHalf + 1024 * i);
+        dma16(vc, off[i], to + R::kCodes + h * kHalf + 1024 * i);
       }
     }
-    s.kp[h] = load_at<u32x4_t>(c.k_pairs + a.slot[h], lo.p);
-  }
-}
-template <int D>
-__device__ __forceinline__ void load_values(StepData<D>& s, const Kv4CacheArg& c, const StepAt& a,
-                                            const LaneOffsets& lo) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint8_t* vc = c.v_codes + a.slot[h] * (D / 2);
-    s.vp[h] = load_at<u32x4_t>(c.v_pairs + a.slot[h], lo.p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t off = lo.v + (uint32_t)(i * (D / 2));
-      if constexpr (D == 64) {
-        s.v[h][i][0] = load_at<uint16_t>(vc, off);
-      } else if constexpr (D == 128) {
-        s.v[h][i][0] = load_at<uint32_t>(vc, off);
-      } else {
-        const u32x2_t w = load_at<u32x2_t>(vc, off);
-        s.v[h][i][0] = w[0];
-        s.v[h][i][1] = w[1];
-      }
+    if (lane < 16) {
+      dma4(kp, 4 * lane, to + 2 * R::kCodes + 64 * h);
+      dma4(vp, 4 * lane, to + 2 * R::kCodes + 128 + 64 * h);
     }
   }
 }
@@ -167,12 +176,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_k
     float* __restrict__ part_o, float* __restrict__ part_ml) {
   constexpr int KC = D / 32;  // score products per half
   constexpr int VC = D / 16;  // value products, and codes per lane and key
+  constexpr int VW = D == 64 ? 1 : D / 128;  // words of these
   // fp16 keeps what p s' loses in bf16 (whose range it needs) as a second
   // operand; bf16 results are rounded to the operand's precision anyway
   constexpr bool kSplitP = std::is_same_v<DT, F16T>;
   constexpr float kOffK = U4Score<DT>::kOff, kOffV = U4Mfma<Bf16T>::kOff + kMid;
   constexpr int OS = D + 4;
-  __shared__ float o_lds[kWaves][16][OS];
+  using R = Ring<D>;
+  // the rings, and after the walk the place of the waves' sums
+  union Shared {
+    uint8_t ring[kWaves][R::kStages * R::kStage];
+    float o[kWaves][16][OS];
+  };
+  __shared__ __attribute__((aligned(16))) Shared lds;
   __shared__ float m_lds[kWaves][16 * NT], l_lds[kWaves][16 * NT];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -228,53 +244,77 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_k
     mu[n] = 0.0f;      // the same in log2 units, 0 while it is -inf
     l[n] = cs[n] = 0.0f;
   }
-  const float c1 = fabsf(a.scale) * kLog2e;
-  const float slack = fminf(kSlack / c1, 3e38f);  // any product is within it where the scale is 0
-  const LaneOffsets lane_at = {(uint32_t)(lr * (D / 2) + lg * (D / 8)),
-                               (uint32_t)(4 * lg * (D / 2) + lr * (D / 32)), 16u * lg};
+  // never 0, which would make a hidden score, -inf, NaN; 2^-100 is as good
+  const float c1 = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);
+  const float slack = kSlack / c1;
+  // where the lane reads its part of a stage
+  uint32_t koff[D == 256 ? 2 : 1], voff[4];
+  if constexpr (D == 64) {
+    koff[0] = R::place(lr, lg >> 1) + 8 * (lg & 1);
+  } else {
+#pragma unroll
+    for (int e = 0; e < D / 128; ++e) koff[e] = R::place(lr, lg * (D / 128) + e);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    voff[i] = R::kCodes + R::place(4 * lg + i, lr * (D / 32) / 16) + lr * (D / 32) % 16;
   const u32x4_t onesv = {U4Mfma<Bf16T>::kOne, U4Mfma<Bf16T>::kOne, U4Mfma<Bf16T>::kOne,
                          U4Mfma<Bf16T>::kOne};
-  const int32_t* table = bt.block_table + (int64_t)b * bt.table_width;
+  const TablePtr table = (TablePtr)(bt.block_table + (int64_t)b * bt.table_width);
 
   // one step; the next one's keys are asked for once these are used, and its
   // values likewise, so one set of registers serves both
-  auto step = [&](StepData<D>& s, const StepAt& at, const StepAt& next, bool more, int t) {
-    const bool masked = !(at.ok[0] && at.ok[1]) || t < all_lo || t + kStep > all_hi;
+  auto step = [&](const uint8_t* s, uint32_t have, int t) __attribute__((always_inline)) {
+    // some row of the tile does not see some key of the step
+    const bool masked = have != 3 || t < all_lo || t + kStep > all_hi;
     // scores
     f32x4_t z[NT][2];
+    const auto* pairs = reinterpret_cast<const u32x4_t*>(s + 2 * R::kCodes) + lg;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      uint32_t kw[KC];
+      if constexpr (D == 64) {
+        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(s + koff[0] + h * (8 * D));
+        kw[0] = w[0];
+        kw[1] = w[1];
+      } else {
+#pragma unroll
+        for (int e = 0; e < D / 128; ++e) {
+          const u32x4_t w = *reinterpret_cast<const u32x4_t*>(s + koff[e] + h * (8 * D));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kw[4 * e + i] = w[i];
+        }
+      }
+      const u32x4_t kp = pairs[4 * h];
 #pragma unroll
       for (int n = 0; n < NT; ++n) z[n][h] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < KC; ++k) {
-        const u32x4_t kk = u4_expand8<U4Score<DT>>(s.k[h][k]);
+        const u32x4_t kk = u4_expand8<U4Score<DT>>(kw[k]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) z[n][h] = DT::mfma16(kk, q[n][k], z[n][h]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float ks = u4_s(s.kp[h][i]);
-        const float km = fmaf(-kOffK, ks, u4_m(s.kp[h][i]));
+        const float ks = u4_s(kp[i]), km = fmaf(-kOffK, ks, u4_m(kp[i]));
 #pragma unroll
         for (int n = 0; n < NT; ++n) z[n][h][i] = fmaf(ks, z[n][h][i], km * qsum[n]);
       }
     }
-    if (more) load_keys<D>(s, c, next, lane_at);
+    const u32x4_t vp0[2] = {pairs[8], pairs[12]};
     u32x4_t pb[NT], pl[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      uint32_t vis = 0xFF;
+      u32x4_t vp[2] = {vp0[0], vp0[1]};
       if (masked) {
-        vis = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const bool v = at.ok[h] &&
+            const bool v = (have >> h & 1) &&
                            (uint32_t)(t + 16 * h + 4 * lg + i - row_lo[n]) < (uint32_t)row_n[n];
             z[n][h][i] = v ? z[n][h][i] : -INFINITY;
-            vis |= (v ? 1u : 0u) << (4 * h + i);
+            vp[h][i] = v ? vp[h][i] : 0;  // whatever a hidden key's pair holds
           }
       }
       float top = fmaxf(fmaxf(fmaxf(z[n][0][0], z[n][0][1]), fmaxf(z[n][0][2], z[n][0][3])),
@@ -284,7 +324,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_k
         const float was = m[n] == -INFINITY ? -INFINITY : mu[n];
         m[n] = top;
         mu[n] = top == -INFINITY ? 0.0f : top * c1;
-        const float f = exp2f(was - mu[n]);
+        const float f = __builtin_amdgcn_exp2f(was - mu[n]);
 #pragma unroll
         for (int j = 0; j < VC; ++j)
 #pragma unroll
@@ -299,17 +339,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_k
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float p = __builtin_amdgcn_exp2f(fmaf(z[n][h][i], c1, -mu[n]));
-          float vs = u4_s(s.vp[h][i]), vm = fmaf(kMid, vs, u4_m(s.vp[h][i]));
-          if (masked) {  // whatever a hidden key's pair holds is not read
-            const bool v = vis >> (4 * h + i) & 1;
-            vs = v ? vs : 0.0f;
-            vm = v ? vm : 0.0f;
-            p = v ? p : 0.0f;  // -inf times a scale of 0
-          }
+          const float p = __builtin_amdgcn_exp2f(fmaf(z[n][h][i], c1, -mu[n]));
+          const float vs = u4_s(vp[h][i]);
           l[n] += p;
           ps[h][i] = p * vs;
-          cs[n] = fmaf(p, vm, cs[n]);
+          cs[n] = fmaf(p, fmaf(kMid, vs, u4_m(vp[h][i])), cs[n]);
         }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -323,13 +357,29 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_k
       if constexpr (kSplitP) po[n] = Bf16T::mfma16(onesv, pl[n], po[n]);
     }
     // values: word w of the operand holds keys 2 w, 2 w + 1 of the lane's 8
+    uint32_t vw[2][4][VW];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* p = s + voff[i] + h * (8 * D);
+        if constexpr (D == 64) {
+          vw[h][i][0] = *reinterpret_cast<const uint16_t*>(p);
+        } else if constexpr (D == 128) {
+          vw[h][i][0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+          const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+          vw[h][i][0] = w[0];
+          vw[h][i][1] = w[1];
+        }
+      }
 #pragma unroll
     for (int half = 0; half < VC / 4; ++half) {  // four channels of the lane
       uint32_t x[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t u0 = s.v[w >> 1][2 * (w & 1)][half >> 1],
-                       u1 = s.v[w >> 1][2 * (w & 1) + 1][half >> 1];
+        const uint32_t u0 = vw[w >> 1][2 * (w & 1)][half >> 1],
+                       u1 = vw[w >> 1][2 * (w & 1) + 1][half >> 1];
         x[w] = half & 1 ? perm(u1, u0, 0x07060302u) : perm(u1, u0, 0x05040100u);
       }
 #pragma unroll
@@ -343,22 +393,56 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_k
         }
       }
     }
-    if (more) load_values<D>(s, c, next, lane_at);
   };
 
   constexpr int kStride = kStep * kWaves;
-  int t = t0 + kStep * wave;
-  if (t < t1) {
-    auto find = [&](int at) { return locate(c, table, bt.table_width, head, at, sp.hi); };
-    StepData<D> s;
-    StepAt at = find(t);
-    load_keys<D>(s, c, at, lane_at);
-    load_values<D>(s, c, at, lane_at);
-    for (; t < t1; t += kStride) {
-      const bool more = t + kStride < t1;
-      const StepAt next = find(more ? t + kStride : t);
-      step(s, at, next, more, t);
-      at = next;
+  const int first = t0 + kStep * wave;
+  if (first < t1) {
+    // One iteration: asks for the stage kAhead steps ahead, waits until this
+    // step's stage is there (loads return in order, so the number that may be
+    // outstanding says so) and works on it.  The stage read and the one being
+    // filled are distinct, which the restrict pointers say: the compiler
+    // leaves the DMA in flight across the reads.  The stage that is filled was
+    // read in the iteration before, whose reads have returned.  The walk
+    // starts kAhead steps early, without work, so that there is one place
+    // that asks: a second would not be known to be distinct.
+    constexpr int kAhead = R::kStages - 1;
+    auto pages_of = [&](int at) { return look_up(c, table, bt.table_width, at, sp.hi); };
+    StepPages pg = pages_of(first);
+    uint32_t have = 0;  // two bits for each step that is in flight, this one's lowest
+    auto iteration = [&](const uint8_t* __restrict__ rd, uint8_t* __restrict__ fill, int t)
+                         __attribute__((always_inline)) {
+      const int at = t + kAhead * kStride;
+      if (at < t1) {
+        const uint32_t h = there(c, pg);
+        have |= h << (2 * kAhead);
+        fetch<D>(c, pg, h, head, at, fill, lane);
+        pg = pages_of(at + kStride);  // for the next time
+        __builtin_amdgcn_s_waitcnt(wait_vm(kAhead * R::kAll));
+      } else if (kAhead == 2 && t + kStride < t1) {
+        __builtin_amdgcn_s_waitcnt(wait_vm(R::kAll));
+      } else {
+        __builtin_amdgcn_s_waitcnt(wait_vm(0));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (t >= first) step(rd, have & 3, t);
+      __builtin_amdgcn_sched_barrier(0);
+      have >>= 2;
+    };
+    uint8_t *const S0 = lds.ring[wave], *const S1 = S0 + R::kStage,
+            *const S2 = S0 + kAhead * R::kStage;
+    // a copy for each place in the ring: with the stages at constant offsets
+    // the compiler knows the age of the DMA that a read has to wait for
+    int t = first - kAhead * kStride;
+    for (;;) {
+      iteration(S1, S0, t);
+      if ((t += kStride) >= t1) break;
+      if constexpr (R::kStages == 3) {
+        iteration(S2, S1, t);
+        if ((t += kStride) >= t1) break;
+      }
+      iteration(S0, S2, t);
+      if ((t += kStride) >= t1) break;
     }
   }
 
@@ -392,7 +476,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_k
         f32x4_t v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = (o[n][j + e][i] + add) * f;
-        *reinterpret_cast<f32x4_t*>(&o_lds[wave][lr][lg * (D / 4) + i * VC + j]) = v;
+        *reinterpret_cast<f32x4_t*>(&lds.o[wave][lr][lg * (D / 4) + i * VC + j]) = v;
       }
     __syncthreads();
     for (int e = threadIdx.x; e < 16 * (D / 4); e += 64 * kWaves) {
@@ -409,7 +493,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_k
       }
       f32x4_t v = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(&o_lds[w][rr][d]);
+      for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(&lds.o[w][rr][d]);
       if (whole) {
         const int i = r / group, hq = head * group + r - i * group;
         const int64_t at = (sq.row0 + i) * a.q_heads + hq;
@@ -458,8 +542,10 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(
     if (mine) {
       const int64_t base =
           (((int64_t)b * c.kv_heads + head) * tiles + tile) * splits * tile_rows + rr;
+#pragma unroll 4
       for (int s = j; s < sp.n; s += J)
         top = fmaxf(top, part_ml[2 * (base + (int64_t)s * tile_rows)]);
+#pragma unroll 4
       for (int s = j; s < sp.n; s += J) {
         const int64_t at = base + (int64_t)s * tile_rows;
         const float ms = part_ml[2 * at], f = ms == -INFINITY ? 0.0f : exp2f(ms - top);
