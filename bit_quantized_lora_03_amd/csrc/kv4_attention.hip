@@ -171,7 +171,7 @@ __device__ __forceinline__ float column_max(float v) {
 }
 
 template <class DT, int D, int NT>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void kv4_attention_kernel(
+__global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attention_kernel(
     Kv4CacheArg c, Kv4BatchArg bt, Kv4AttnArg a, int chunk, int splits, int tiles,
     float* __restrict__ part_o, float* __restrict__ part_ml) {
   constexpr int KC = D / 32;  // score products per half
@@ -589,8 +589,13 @@ void go(const Kv4CacheArg& c, const Kv4BatchArg& b, const Kv4AttnArg& a, const K
   const int64_t parts = (int64_t)b.seqs * c.kv_heads * p.tiles * p.splits * p.tile;
   float* ml = ws ? ws + parts * D : nullptr;
   const dim3 grid((unsigned)(p.splits * p.tiles), (unsigned)c.kv_heads, (unsigned)b.seqs);
-  kv4_attention_kernel<DT, D, 1>
-      <<<grid, 64 * kWaves, 0, s>>>(c, b, a, p.chunk, p.splits, p.tiles, ws, ml);
+  auto walk = [&](auto nt) {
+    kv4_attention_kernel<DT, D, decltype(nt)::value>
+        <<<grid, 64 * kWaves, 0, s>>>(c, b, a, p.chunk, p.splits, p.tiles, ws, ml);
+  };
+  if (p.tile == 16) walk(std::integral_constant<int, 1>{});
+  if constexpr (D == 128)
+    if (p.tile == 32) walk(std::integral_constant<int, 2>{});
   if (p.splits > 1) {
     const int64_t rows = (int64_t)b.max_q * (a.q_heads / c.kv_heads);
     auto join = [&](auto jc) {
@@ -611,13 +616,13 @@ void go(const Kv4CacheArg& c, const Kv4BatchArg& b, const Kv4AttnArg& a, const K
 Kv4AttnPlan kv4_attn_plan(int64_t seqs, int64_t max_q, int64_t max_len, int q_heads, int kv_heads,
                           int head_dim, int window) {
   Kv4AttnPlan p;
-  p.tile = 16;
   const int64_t rows = max_q * (q_heads / kv_heads);
+  p.tile = head_dim == 128 && rows >= 64 ? 32 : 16;
   p.tiles = (int)((rows + p.tile - 1) / p.tile);
   int64_t keys = max_len;
   // a tile's window starts up to 31 keys early
   if (window > 0 && window + max_q + kStep < keys) keys = window + max_q + kStep;
-  const int64_t want = 4096, base = seqs * kv_heads * p.tiles;
+  const int64_t want = 1536, base = seqs * kv_heads * p.tiles;
   const int64_t per = kStep * kWaves;
   int64_t chunk = (keys * base + want - 1) / want;
   chunk = (chunk + per - 1) / per * per;

@@ -10,18 +10,36 @@ before the library is called; what the library itself refuses raises
 
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Tuple
 
 import torch
 
 from . import _lib
-from ._lib import Kv4BatchStruct, Kv4CacheStruct, QloraError, U4Struct, check
+from ._lib import Kv4BatchStruct, Kv4CacheStruct, QloraError, U4Struct
 
 GROUPS = (32, 64, 128)
 HEAD_DIMS = (64, 128, 256)
 _16BIT = {torch.bfloat16: "", torch.float16: "_f16"}
 _u8, _i32, _f32, _bf16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+_current = torch._C._cuda_getDevice
+_stream = torch._C._cuda_getCurrentRawStream
+_entry = {}
+
+
+def _call(name: str, dtype, index: int, *args) -> None:
+    """Calls the entry point (its fp16 form where ``dtype`` is fp16) with
+    ``args`` and the current stream of GPU ``index``, which is the current
+    device meanwhile."""
+    f = _entry.get((name, dtype))
+    if f is None:
+        f = _entry[name, dtype] = getattr(_lib.lib(), name + _16BIT.get(dtype, ""))
+    if _current() == index:
+        st = f(*args, _stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, _stream(index))
+    if st:
+        raise QloraError(st, name + _16BIT.get(dtype, ""))
 
 
 def _need(ok: bool, what: str) -> None:
@@ -29,34 +47,16 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _dense(t, name: str, dtype, device=None) -> None:
+def _dense(t, name: str, dtype, index: int = -1) -> None:
+    at = t.get_device()
     if t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
-    if not t.is_cuda:
+    if at < 0:
         raise ValueError(f"{name}: a tensor on the GPU is needed")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the others on {device}")
+    if index >= 0 and at != index:
+        raise ValueError(f"{name}: on {t.device}, the others on GPU {index}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: has to be contiguous")
-
-
-class _On:
-    """Makes ``device`` the current one for a call if it is not already, and
-    gives the raw handle of its current stream."""
-    __slots__ = ("index", "was")
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.index != self.was:
-            torch.cuda.set_device(self.index)
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        if self.index != self.was:
-            torch.cuda.set_device(self.was)
 
 
 # ---------------------------------------------------------------------------
@@ -68,20 +68,25 @@ class U4Weight:
     (even element in the low nibble) and ``pairs`` bf16 [N, K/group, 2] (s
     and m; a value is m + s * code)."""
 
-    __slots__ = ("codes", "pairs", "N", "K", "group", "device", "struct")
+    __slots__ = ("codes", "pairs", "N", "K", "group", "index", "struct")
 
     def __init__(self, codes, pairs):
         _dense(codes, "codes", _u8)
-        _dense(pairs, "pairs", _bf16, codes.device)
-        _need(codes.dim() == 2 and pairs.dim() == 3 and pairs.shape[0] == codes.shape[0]
-              and pairs.shape[2] == 2 and pairs.shape[1] > 0,
-              "codes [N, K/2] and pairs [N, K/group, 2] are needed")
-        self.N, half = codes.shape
-        self.K, self.group = 2 * half, 2 * half // pairs.shape[1]
-        _need(self.group in GROUPS and self.group * pairs.shape[1] == self.K,
-              f"groups of {GROUPS} values are supported")
-        self.codes, self.pairs, self.device = codes, pairs, codes.device
-        self.struct = U4Struct(codes.data_ptr(), pairs.data_ptr(), self.N, self.K, self.group)
+        self.index = codes.get_device()
+        _dense(pairs, "pairs", _bf16, self.index)
+        cs, ps = codes.shape, pairs.shape
+        if len(cs) != 2 or len(ps) != 3 or ps[0] != cs[0] or ps[2] != 2 or ps[1] == 0:
+            raise ValueError("codes [N, K/2] and pairs [N, K/group, 2] are needed")
+        self.N, self.K = N, K = cs[0], 2 * cs[1]
+        self.group = group = K // ps[1]
+        if group not in GROUPS or group * ps[1] != K:
+            raise ValueError(f"groups of {GROUPS} values are supported")
+        self.codes, self.pairs = codes, pairs
+        self.struct = U4Struct(codes.data_ptr(), pairs.data_ptr(), N, K, group)
+
+    @property
+    def device(self):
+        return self.codes.device
 
 
 def quantize_u4(w, group: int = 64) -> U4Weight:
@@ -92,11 +97,11 @@ def quantize_u4(w, group: int = 64) -> U4Weight:
     N, K = w.shape
     _need(N > 0 and K > 0 and K % group == 0, f"K = {K} is not a positive multiple of {group}")
     w = w.contiguous()
-    codes = torch.empty((N, K // 2), dtype=_u8, device=w.device)
-    pairs = torch.empty((N, K // group, 2), dtype=_bf16, device=w.device)
-    with _On(w.device) as s:
-        check(_lib.lib().qlora_quantize_u4(w.data_ptr(), N * K, group, codes.data_ptr(),
-                                           pairs.data_ptr(), s), "qlora_quantize_u4")
+    device = w.device
+    codes = torch.empty((N, K // 2), dtype=_u8, device=device)
+    pairs = torch.empty((N, K // group, 2), dtype=_bf16, device=device)
+    _call("qlora_quantize_u4", None, w.get_device(), w.data_ptr(), N * K, group, codes.data_ptr(),
+          pairs.data_ptr())
     return U4Weight(codes, pairs)
 
 
@@ -104,35 +109,29 @@ def dequantize_u4(uw: U4Weight, dtype=torch.bfloat16):
     """U4Weight -> its values [N, K] in bf16 or fp16."""
     _need(dtype in _16BIT, "bf16 or fp16 values")
     out = torch.empty((uw.N, uw.K), dtype=dtype, device=uw.device)
-    name = "qlora_dequantize_u4" + _16BIT[dtype]
-    with _On(uw.device) as s:
-        check(getattr(_lib.lib(), name)(ctypes.byref(uw.struct), out.data_ptr(), s), name)
+    _call("qlora_dequantize_u4", dtype, uw.index, uw.struct, out.data_ptr())
     return out
 
 
 def linear_u4_fwd(uw: U4Weight, x, y=None):
     """y = x . W^T for few tokens: x [M, K] bf16 or fp16 (rows may be
     strided), y [M, N] of the same type (rows may be strided)."""
-    tail = _16BIT.get(x.dtype)
-    _need(tail is not None, "x has to be bf16 or fp16")
-    _need(x.dim() == 2 and x.shape[1] == uw.K and x.device == uw.device and x.stride(1) == 1,
-          f"x: [M, {uw.K}] on {uw.device} with unit stride along K is needed")
-    M = x.shape[0]
+    dt, shape, N, K, index = x.dtype, x.shape, uw.N, uw.K, uw.index
+    if dt not in _16BIT:
+        raise ValueError("x has to be bf16 or fp16")
+    if len(shape) != 2 or shape[1] != K or x.get_device() != index or x.stride(1) != 1:
+        raise ValueError(f"x: [M, {K}] on GPU {index} with unit stride along K is needed")
+    M = shape[0]
     if y is None:
-        y = torch.empty((M, uw.N), dtype=x.dtype, device=uw.device)
-        ldy = uw.N
+        y = torch.empty((M, N), dtype=dt, device=x.device)
+        ldy = N
     else:
-        _need(y.dtype is x.dtype and tuple(y.shape) == (M, uw.N) and y.device == uw.device
-              and (y.stride(1) == 1 or uw.N == 1),
-              f"y: [{M}, {uw.N}] like x, with unit stride along N, is needed")
-        ldy = y.stride(0) if M > 1 else max(uw.N, y.stride(0))
-    ldx = x.stride(0) if M > 1 else uw.K
-    lib = _lib.lib()
-    f = lib.qlora_linear_u4_fwd_f16 if tail else lib.qlora_linear_u4_fwd
-    with _On(uw.device) as s:
-        st = f(uw.struct, x.data_ptr(), ldx, M, y.data_ptr(), ldy, s)
-    if st:
-        raise QloraError(st, "qlora_linear_u4_fwd" + tail)
+        _need(y.dtype is dt and tuple(y.shape) == (M, N) and y.get_device() == index
+              and (y.stride(1) == 1 or N == 1),
+              f"y: [{M}, {N}] like x, with unit stride along N, is needed")
+        ldy = y.stride(0) if M > 1 else N
+    _call("qlora_linear_u4_fwd", dt, index, uw.struct, x.data_ptr(), x.stride(0) if M > 1 else K,
+          M, y.data_ptr(), ldy)
     return y
 
 
@@ -146,26 +145,33 @@ class Kv4Cache:
     kv_heads, page_size, 2], one pair per token and head."""
 
     __slots__ = ("k_codes", "k_pairs", "v_codes", "v_pairs", "pages", "kv_heads", "page_size",
-                 "head_dim", "device", "struct")
+                 "head_dim", "index", "struct")
 
     def __init__(self, k_codes, k_pairs, v_codes, v_pairs):
-        self.device = k_codes.device
-        for t, n, dt in ((k_codes, "k_codes", _u8), (k_pairs, "k_pairs", _bf16),
-                         (v_codes, "v_codes", _u8), (v_pairs, "v_pairs", _bf16)):
-            _dense(t, n, dt, self.device)
-        _need(k_codes.dim() == 4, "codes [pages, kv_heads, page_size, head_dim / 2] are needed")
-        self.pages, self.kv_heads, self.page_size, half = k_codes.shape
+        _dense(k_codes, "k_codes", _u8)
+        self.index = index = k_codes.get_device()
+        _dense(k_pairs, "k_pairs", _bf16, index)
+        _dense(v_codes, "v_codes", _u8, index)
+        _dense(v_pairs, "v_pairs", _bf16, index)
+        shape = k_codes.shape
+        if len(shape) != 4:
+            raise ValueError("codes [pages, kv_heads, page_size, head_dim / 2] are needed")
+        self.pages, self.kv_heads, self.page_size, half = pages, heads, size, half = shape
         self.head_dim = 2 * half
-        pair = (self.pages, self.kv_heads, self.page_size, 2)
-        _need(v_codes.shape == k_codes.shape and tuple(k_pairs.shape) == pair
-              and tuple(v_pairs.shape) == pair, "codes and pairs of one cache differ in shape")
-        _need(self.head_dim in HEAD_DIMS, f"head_dim {self.head_dim}: {HEAD_DIMS} are supported")
-        _need(16 <= self.page_size <= 1024 and self.page_size & (self.page_size - 1) == 0,
-              f"page_size {self.page_size}: a power of two from 16 to 1024 is needed")
+        pair = (pages, heads, size, 2)
+        if v_codes.shape != shape or k_pairs.shape != pair or v_pairs.shape != pair:
+            raise ValueError("codes and pairs of one cache differ in shape")
+        if 2 * half not in HEAD_DIMS:
+            raise ValueError(f"head_dim {2 * half}: {HEAD_DIMS} are supported")
+        if not 16 <= size <= 1024 or size & (size - 1):
+            raise ValueError(f"page_size {size}: a power of two from 16 to 1024 is needed")
         self.k_codes, self.k_pairs, self.v_codes, self.v_pairs = k_codes, k_pairs, v_codes, v_pairs
         self.struct = Kv4CacheStruct(k_codes.data_ptr(), k_pairs.data_ptr(), v_codes.data_ptr(),
-                                     v_pairs.data_ptr(), self.pages, self.page_size,
-                                     self.kv_heads, self.head_dim)
+                                     v_pairs.data_ptr(), pages, size, heads, 2 * half)
+
+    @property
+    def device(self):
+        return self.k_codes.device
 
     @classmethod
     def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
@@ -176,32 +182,35 @@ class Kv4Cache:
 
 
 def _batch(cache: Kv4Cache, cu_q, seq_lens, block_table, max_q: int, rows: int) -> Kv4BatchStruct:
+    index = cache.index
     for t, n in ((cu_q, "cu_q"), (seq_lens, "seq_lens"), (block_table, "block_table")):
-        if t.dtype is not _i32 or t.device != cache.device or not t.is_contiguous():
-            raise ValueError(f"{n}: a contiguous int32 tensor on {cache.device} is needed")
-    B = seq_lens.shape[0]
-    if cu_q.dim() != 1 or cu_q.shape[0] != B + 1 or seq_lens.dim() != 1 or \
-            block_table.dim() != 2 or block_table.shape[0] != B:
+        if t.dtype is not _i32 or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{n}: a contiguous int32 tensor on GPU {index} is needed")
+    cs, ls, bs = cu_q.shape, seq_lens.shape, block_table.shape
+    if len(ls) != 1 or len(cs) != 1 or len(bs) != 2 or cs[0] != ls[0] + 1 or bs[0] != ls[0]:
         raise ValueError("cu_q [B + 1], seq_lens [B] and block_table [B, width] are needed")
     if max_q < 0:
         raise ValueError("max_q is negative")
-    return Kv4BatchStruct(cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), rows, B,
-                          block_table.shape[1], max_q)
+    return Kv4BatchStruct(cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), rows,
+                          ls[0], bs[1], max_q)
 
 
-def _rows(cache: Kv4Cache, t, name: str, dtype, rows: Optional[int], heads: Optional[int]):
-    """Checks a [T, heads, head_dim] tensor; returns its (token, head) strides."""
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or t.dtype is not dtype or \
-            t.device != cache.device or (rows is not None and t.shape[0] != rows) or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name}: [{'T' if rows is None else rows}, "
-                         f"{'heads' if heads is None else heads}, {cache.head_dim}] of {dtype} on "
-                         f"{cache.device} is needed, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+def _rows(cache: Kv4Cache, t, name: str, dtype, rows: int, heads: int):
+    """Checks a [rows, heads, head_dim] tensor (-1: any); returns its rows,
+    heads and (token, head) strides."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or t.dtype is not dtype or \
+            t.get_device() != cache.index or (rows >= 0 and shape[0] != rows) or \
+            (heads >= 0 and shape[1] != heads):
+        raise ValueError(f"{name}: [{'T' if rows < 0 else rows}, "
+                         f"{'heads' if heads < 0 else heads}, {cache.head_dim}] of {dtype} on "
+                         f"{cache.device} is needed, got {tuple(shape)} of {t.dtype} on {t.device}")
     ts, hs, ds = t.stride()
     if ds != 1:
         raise ValueError(f"{name}: unit stride along head_dim is needed")
     # the stride of an axis of length one says nothing
-    return (ts if t.shape[0] > 1 else 0), (hs if t.shape[1] > 1 else 0)
+    T, H = shape[0], shape[1]
+    return T, H, (ts if T > 1 else 0), (hs if H > 1 else 0)
 
 
 def kv4_append(cache: Kv4Cache, k, v, cu_q, seq_lens, block_table, max_q: int, q=None,
@@ -215,20 +224,18 @@ def kv4_append(cache: Kv4Cache, k, v, cu_q, seq_lens, block_table, max_q: int, q
     length with them is seq_lens[b]; block_table [B, width] names its pages;
     no sequence has more than ``max_q`` rows."""
     dt = k.dtype
-    tail = _16BIT.get(dt)
-    _need(tail is not None, "k, v and q have to be bf16 or fp16")
-    T = k.shape[0] if k.dim() else 0
-    kts, khs = _rows(cache, k, "k", dt, None, cache.kv_heads)
-    vts, vhs = _rows(cache, v, "v", dt, T, cache.kv_heads)
+    if dt not in _16BIT:
+        raise ValueError("k, v and q have to be bf16 or fp16")
+    T, _, kts, khs = _rows(cache, k, "k", dt, -1, cache.kv_heads)
+    _, _, vts, vhs = _rows(cache, v, "v", dt, T, cache.kv_heads)
     qp = op = None
     qts = qhs = heads = 0
     if q is not None:
-        qts, qhs = _rows(cache, q, "q", dt, T, None)
-        heads = q.shape[1]
+        _, heads, qts, qhs = _rows(cache, q, "q", dt, T, -1)
         if q_out is None:
-            q_out = torch.empty((T, heads, cache.head_dim), dtype=dt, device=cache.device)
+            q_out = torch.empty((T, heads, cache.head_dim), dtype=dt, device=k.device)
         else:
-            _need(q_out.shape == q.shape and q_out.dtype is dt and q_out.device == cache.device
+            _need(q_out.shape == q.shape and q_out.dtype is dt and q_out.get_device() == cache.index
                   and q_out.is_contiguous(), "q_out has to be contiguous and like q")
         qp, op = q.data_ptr(), q_out.data_ptr()
     else:
@@ -237,17 +244,12 @@ def kv4_append(cache: Kv4Cache, k, v, cu_q, seq_lens, block_table, max_q: int, q
     tp = None
     if cos_sin is not None:
         _need(cos_sin.dim() == 2, "cos_sin: [positions, rot] is needed")
-        _dense(cos_sin, "cos_sin", _f32, cache.device)
+        _dense(cos_sin, "cos_sin", _f32, cache.index)
         rows, rot = cos_sin.shape
         tp = cos_sin.data_ptr()
     bt = _batch(cache, cu_q, seq_lens, block_table, max_q, T)
-    lib = _lib.lib()
-    f = lib.qlora_kv4_append_f16 if tail else lib.qlora_kv4_append
-    with _On(cache.device) as s:
-        st = f(cache.struct, bt, k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs, qp, qts, qhs,
-               heads, tp, rows, rot, 1 if interleaved else 0, op, s)
-    if st:
-        raise QloraError(st, "qlora_kv4_append" + tail)
+    _call("qlora_kv4_append", dt, cache.index, cache.struct, bt, k.data_ptr(), kts, khs,
+          v.data_ptr(), vts, vhs, qp, qts, qhs, heads, tp, rows, rot, 1 if interleaved else 0, op)
     return q_out
 
 
@@ -256,19 +258,13 @@ def kv4_read(cache: Kv4Cache, cu_q, seq_lens, block_table, max_q: int, rows: int
     """The keys and values that the cache holds for the batch's ``rows`` rows,
     [rows, kv_heads, head_dim] each, in bf16 or fp16; rows behind
     cu_q[-1] are uninitialised."""
-    tail = _16BIT.get(dtype)
-    _need(tail is not None, "bf16 or fp16 values")
+    _need(dtype in _16BIT, "bf16 or fp16 values")
     _need(rows >= 0, "rows is negative")
     bt = _batch(cache, cu_q, seq_lens, block_table, max_q, rows)
-    shape = (rows, cache.kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=cache.device)
-    v = torch.empty(shape, dtype=dtype, device=cache.device)
-    lib = _lib.lib()
-    f = lib.qlora_kv4_read_f16 if tail else lib.qlora_kv4_read
-    with _On(cache.device) as s:
-        st = f(cache.struct, bt, k.data_ptr(), v.data_ptr(), s)
-    if st:
-        raise QloraError(st, "qlora_kv4_read" + tail)
+    shape, device = (rows, cache.kv_heads, cache.head_dim), cu_q.device
+    k = torch.empty(shape, dtype=dtype, device=device)
+    v = torch.empty(shape, dtype=dtype, device=device)
+    _call("qlora_kv4_read", dtype, cache.index, cache.struct, bt, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -287,36 +283,31 @@ def kv4_attention(cache: Kv4Cache, q, cu_q, seq_lens, block_table, max_q: int, m
     is longer than ``max_len``; a row at position p sees keys up to p
     (``causal``) and after p - window (``window`` > 0)."""
     dt = q.dtype
-    tail = _16BIT.get(dt)
-    _need(tail is not None, "q has to be bf16 or fp16")
-    qts, qhs = _rows(cache, q, "q", dt, None, None)
-    T, heads, D = q.shape
+    if dt not in _16BIT:
+        raise ValueError("q has to be bf16 or fp16")
+    T, heads, qts, qhs = _rows(cache, q, "q", dt, -1, -1)
+    D, index, device = cache.head_dim, cache.index, q.device
     bt = _batch(cache, cu_q, seq_lens, block_table, max_q, T)
     if out is None:
-        out = torch.empty((T, heads, D), dtype=dt, device=cache.device)
+        out = torch.empty((T, heads, D), dtype=dt, device=device)
     else:
-        _need(out.shape == q.shape and out.dtype is dt and out.device == cache.device
+        _need(out.shape == q.shape and out.dtype is dt and out.get_device() == index
               and out.is_contiguous(), "out has to be contiguous and like q")
     if lse is not None:
         _need(tuple(lse.shape) == (T, heads) and lse.dtype is _f32 and lse.is_contiguous()
-              and lse.device == cache.device, f"lse: fp32 [{T}, {heads}] is needed")
+              and lse.get_device() == index, f"lse: fp32 [{T}, {heads}] is needed")
     elif return_lse:
-        lse = torch.empty((T, heads), dtype=_f32, device=cache.device)
-    lib = _lib.lib()
-    need = lib.qlora_kv4_attention_workspace_bytes(bt.seqs, max_q, max_len, heads, cache.kv_heads,
-                                                   D, window)
+        lse = torch.empty((T, heads), dtype=_f32, device=device)
+    need = _lib.lib().qlora_kv4_attention_workspace_bytes(bt.seqs, max_q, max_len, heads,
+                                                          cache.kv_heads, D, window)
     if workspace is None:
         if need:
-            workspace = torch.empty(need, dtype=_u8, device=cache.device)
+            workspace = torch.empty(need, dtype=_u8, device=device)
     else:
-        _dense(workspace, "workspace", _u8, cache.device)
+        _dense(workspace, "workspace", _u8, index)
         need = workspace.numel()
-    f = lib.qlora_kv4_attention_f16 if tail else lib.qlora_kv4_attention
-    with _On(cache.device) as s:
-        st = f(cache.struct, bt, q.data_ptr(), qts, qhs, heads,
-               D ** -0.5 if scale is None else scale, 1 if causal else 0, window, max_len,
-               out.data_ptr(), None if lse is None else lse.data_ptr(),
-               None if workspace is None else workspace.data_ptr(), need, s)
-    if st:
-        raise QloraError(st, "qlora_kv4_attention" + tail)
+    _call("qlora_kv4_attention", dt, index, cache.struct, bt, q.data_ptr(), qts, qhs, heads,
+          D ** -0.5 if scale is None else scale, 1 if causal else 0, window, max_len,
+          out.data_ptr(), None if lse is None else lse.data_ptr(),
+          None if workspace is None else workspace.data_ptr(), need)
     return (out, lse) if return_lse else out
