@@ -175,7 +175,7 @@ int append(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, const uin
       if (!q_out) return QLORA_EINVAL;
       if (!aligned(q_out, 16)) return QLORA_EALIGN;
     }
-    if ((int64_t)b.max_q * (q_heads + 2 * c.kv_heads) / 4 > kMaxGrid) return QLORA_ESHAPE;
+    if ((int64_t)b.max_q * (q_heads + 2 * c.kv_heads) > kMaxGrid) return QLORA_ESHAPE;
     const size_t cb = code_bytes(cache), pb = pair_bytes(cache);
     if (clash<5, 7>({{c.k_codes, cb},
                      {c.v_codes, cb},
@@ -209,7 +209,7 @@ int read(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, uint16_t* k
     if (no_rows(batch)) return QLORA_OK;
     if (!k_out || !v_out) return QLORA_EINVAL;
     if (!aligned(k_out, 16) || !aligned(v_out, 16)) return QLORA_EALIGN;
-    if ((int64_t)b.max_q * 2 * c.kv_heads / 4 > kMaxGrid) return QLORA_ESHAPE;
+    if ((int64_t)b.max_q * 2 * c.kv_heads > kMaxGrid) return QLORA_ESHAPE;
     const size_t cb = code_bytes(cache), pb = pair_bytes(cache),
                  no = (size_t)b.rows * c.kv_heads * c.head_dim * 2;
     if (clash<2, 7>({{k_out, no}, {v_out, no}},

@@ -5,11 +5,15 @@
 // [page size][head_dim / 2] and pairs [pages][kv heads][page size]: one
 // group of the 4-bit format (u4_common.h) per token and head.
 //
-// Both kernels move little data per token and are bound by latency at a
-// decode step and by HBM at a prefill.  A head's vector is D / 8
-// neighbouring lanes with 8 values each, every vector of a call is
-// independent, and a token's sequence comes from the grid (y), so no lane
-// searches for it.
+// Both are bound by latency at a decode step and by HBM at a prefill.  A
+// head's vector is D / 8 neighbouring lanes with 8 values each, every vector
+// of a call is independent, and a token's sequence comes from the grid (y), so
+// no lane searches for it.  Several vectors for each lane, asked for together,
+// were no faster (43 against 40 us).
+//
+// Measured: 64 new tokens of 32 + 2 x 8 heads, D 128, bf16: 4.0 us, the read
+// 3.0; 6600 tokens of them, fp16: 40 us (a copy of the same bytes takes 30),
+// the read 9.5.
 
 #include "kv4_common.h"
 #include "launch.h"
@@ -19,41 +23,70 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One 16-bit head vector: where this lane's two runs of four values start.
-// The rotated pairs lie in one lane: (i, i + rot / 2) with runs at 4 l and
-// rot / 2 + 4 l, or neighbours (interleaved, and past the rotated part)
-// with one run of 8.
+// One head vector is D / 8 lanes.  A lane has two runs of four values, which
+// start at a and b: where it rotates pairs (i, i + rot / 2), at 4 l and
+// rot / 2 + 4 l, so that it has both of a pair; else (no rotation, rotation
+// of neighbours, and past the rotated part) they are one run of 8.
 struct Runs {
   int a, b;
 };
-__device__ __forceinline__ Runs lane_runs(int l, int rot, int interleaved) {
-  const int rl = rot >> 3;  // lanes that rotate
-  if (l < rl && !interleaved) return {4 * l, (rot >> 1) + 4 * l};
+__device__ __forceinline__ Runs lane_runs(int l, int rot, bool halves) {
+  if (halves && l < rot >> 3) return {4 * l, (rot >> 1) + 4 * l};
   return {8 * l, 8 * l + 4};
 }
 
 template <class DT>
-__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[8], int at) {
-  const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+__device__ __forceinline__ void unpack4(u32x2_t w, float (&v)[8], int at) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[at + i] = DT::tof((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
 }
 
-// Positions and places are worked out per vector; rotation and encoding run
-// in fp64 (half the fp32 rate on this chip, and a few operations a value):
-// a product of a 16-bit value and an fp32 cosine is exact there and the
-// rotated value rounded once, so codes at a border come out as defined.
+// Codes and pair of a head vector of T (fp32: as loaded; fp64: rotated), into
+// its place in the cache.
+template <int D, class T>
+__device__ __forceinline__ void encode(const T (&v)[8], Runs r, bool halves, int l, int64_t slot,
+                                       uint8_t* codes, uint32_t* pairs) {
+  T lo = v[0], hi = v[0];
+  bool fin = true;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    lo = v[j] < lo ? v[j] : lo;
+    hi = v[j] > hi ? v[j] : hi;
+    fin = fin && fabs(v[j]) <= (T)3.4028234663852886e38;
+  }
+  lanes_minmax<D / 8>(lo, hi);
+  const U4Coder u = u4_coder<T>(lo, hi, lanes_all<D / 8>(fin));
+  uint32_t ca = 0, cb = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    ca |= u4_code(u, v[j], (float)(v[j] - (T)u.m)) << (4 * j);
+    cb |= u4_code(u, v[j + 4], (float)(v[j + 4] - (T)u.m)) << (4 * j);
+  }
+  if (slot < 0) return;
+  uint8_t* c = codes + slot * (D / 2);
+  if (!halves) {
+    *reinterpret_cast<uint32_t*>(c + r.a / 2) = ca | cb << 16;
+  } else {
+    *reinterpret_cast<uint16_t*>(c + r.a / 2) = (uint16_t)ca;
+    *reinterpret_cast<uint16_t*>(c + r.b / 2) = (uint16_t)cb;
+  }
+  if (l == 0) pairs[slot] = u.pair;
+}
+
+// Rotation runs in fp64 (a few operations a value at fp32's rate): a product
+// of a 16-bit value and an fp32 cosine is exact there and the rotated value
+// is rounded once, so codes at a border come out as defined.
 template <class DT, int D>
 __global__ __launch_bounds__(kThreads) void kv4_append_kernel(Kv4CacheArg c, Kv4BatchArg bt,
                                                               Kv4AppendArg a) {
   constexpr int LPV = D / 8, VPB = kThreads / LPV;
   const int l = threadIdx.x % LPV;
-  const int64_t v = (int64_t)blockIdx.x * VPB + threadIdx.x / LPV;
-  const int heads = a.q_heads + 2 * c.kv_heads;
+  const uint32_t v = blockIdx.x * VPB + threadIdx.x / LPV;
+  const uint32_t heads = a.q_heads + 2 * c.kv_heads;
   const int b = blockIdx.y;
   const Kv4Seq sq = kv4_seq(bt, b);
-  const int64_t i = v / heads;
-  int h = (int)(v - i * heads);
+  const int i = v / heads;
+  int h = v - i * heads;
   if (i >= sq.n) return;
   const int64_t row = sq.row0 + i, pos = sq.pos0 + i;
   const bool is_q = h < a.q_heads;
@@ -62,65 +95,67 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(Kv4CacheArg c, Kv4
   if (is_v) h -= c.kv_heads;
 
   const int rot = is_v ? 0 : a.rot;
-  const Runs r = lane_runs(l, rot, a.interleaved);
-  const uint16_t* src = is_q ? a.q + row * a.q_ts + h * a.q_hs
-                             : is_v ? a.v + row * a.v_ts + h * a.v_hs
-                                    : a.k + row * a.k_ts + h * a.k_hs;
+  const bool halves = rot > 0 && !a.interleaved;
+  const Runs r = lane_runs(l, rot, halves);
+  const uint16_t* src = is_q   ? a.q + row * a.q_ts + h * a.q_hs
+                        : is_v ? a.v + row * a.v_ts + h * a.v_hs
+                               : a.k + row * a.k_ts + h * a.k_hs;
   float x[8];
-  load4<DT>(src + r.a, x, 0);
-  load4<DT>(src + r.b, x, 4);
+  if (!halves) {
+    const u32x4_t w = *reinterpret_cast<const u32x4_t*>(src + r.a);
+    unpack4<DT>(u32x2_t{w[0], w[1]}, x, 0);
+    unpack4<DT>(u32x2_t{w[2], w[3]}, x, 4);
+  } else {
+    unpack4<DT>(*reinterpret_cast<const u32x2_t*>(src + r.a), x, 0);
+    unpack4<DT>(*reinterpret_cast<const u32x2_t*>(src + r.b), x, 4);
+  }
+  // no angle for this position: the query becomes NaN, nothing is stored
+  const bool known = pos >= 0 && (a.rot == 0 || pos < a.table_rows);
+  if (is_v) {
+    encode<D, float>(x, r, false, l, known ? kv4_slot(c, bt, b, pos, h) : -1, c.v_codes, c.v_pairs);
+    return;
+  }
   double d[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) d[j] = x[j];
-  // no angle for this position: the query becomes NaN, nothing is stored
-  const bool known = a.rot == 0 ? pos >= 0 : (pos >= 0 && pos < a.table_rows);
   if (l < (rot >> 3) && known) {
-    const float* t = a.cos_sin + pos * rot;
-    const int first = 4 * l;  // of the lane's four angles
-    const f32x4_t co = *reinterpret_cast<const f32x4_t*>(t + first);
-    const f32x4_t si = *reinterpret_cast<const f32x4_t*>(t + (rot >> 1) + first);
+    const float* t = a.cos_sin + pos * rot + 4 * l;  // the lane's four angles
+    const f32x4_t co = *reinterpret_cast<const f32x4_t*>(t);
+    const f32x4_t si = *reinterpret_cast<const f32x4_t*>(t + (rot >> 1));
+    auto turn = [&](double& p, double& q, int j) {
+      const double u = p, w = q;
+      p = fma(-w, (double)si[j], u * (double)co[j]);
+      q = fma(u, (double)si[j], w * (double)co[j]);
+    };
+    if (halves) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int p0 = a.interleaved ? 2 * j : j, p1 = a.interleaved ? 2 * j + 1 : j + 4;
-      const double u = d[p0], w = d[p1], cj = co[j], sj = si[j];
-      d[p0] = fma(-w, sj, u * cj);
-      d[p1] = fma(u, sj, w * cj);
+      for (int j = 0; j < 4; ++j) turn(d[j], d[j + 4], j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) turn(d[2 * j], d[2 * j + 1], j);
     }
   }
-  if (is_q) {
-    if (!known) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = __builtin_nan("");
-    }
-    uint16_t* o = a.q_out + (row * a.q_heads + h) * D;
-    *reinterpret_cast<u32x2_t*>(o + r.a) =
-        u32x2_t{DT::pack2((float)d[0], (float)d[1]), DT::pack2((float)d[2], (float)d[3])};
-    *reinterpret_cast<u32x2_t*>(o + r.b) =
-        u32x2_t{DT::pack2((float)d[4], (float)d[5]), DT::pack2((float)d[6], (float)d[7])};
+  if (!is_q) {
+    encode<D, double>(d, r, halves, l, known ? kv4_slot(c, bt, b, pos, h) : -1, c.k_codes,
+                      c.k_pairs);
     return;
   }
-  double lo = d[0], hi = d[0];
-  bool fin = true;
+  // by way of fp32, which the compiler may not see: it knows no instruction
+  // from fp64 to fp16 and writes 35 for each value instead of two
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    lo = d[j] < lo ? d[j] : lo;
-    hi = d[j] > hi ? d[j] : hi;
-    fin = fin && fabs(d[j]) <= 1e300;
+    x[j] = known ? (float)d[j] : __builtin_nanf("");
+    asm("" : "+v"(x[j]));
   }
-  lanes_minmax<LPV>(lo, hi);
-  const U4Coder u = u4_coder(lo, hi, lanes_all<LPV>(fin));
-  uint32_t ca = 0, cb = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    ca |= u4_code(u, d[j], (float)(d[j] - (double)u.m)) << (4 * j);
-    cb |= u4_code(u, d[j + 4], (float)(d[j + 4] - (double)u.m)) << (4 * j);
+  uint16_t* o = a.q_out + (row * a.q_heads + h) * D;
+  const u32x2_t oa = {DT::pack2(x[0], x[1]), DT::pack2(x[2], x[3])};
+  const u32x2_t ob = {DT::pack2(x[4], x[5]), DT::pack2(x[6], x[7])};
+  if (!halves) {
+    *reinterpret_cast<u32x4_t*>(o + r.a) = u32x4_t{oa[0], oa[1], ob[0], ob[1]};
+  } else {
+    *reinterpret_cast<u32x2_t*>(o + r.a) = oa;
+    *reinterpret_cast<u32x2_t*>(o + r.b) = ob;
   }
-  const int64_t slot = known ? kv4_slot(c, bt, b, pos, h) : -1;
-  if (slot < 0) return;
-  uint8_t* codes = (is_v ? c.v_codes : c.k_codes) + slot * (D / 2);
-  *reinterpret_cast<uint16_t*>(codes + r.a / 2) = (uint16_t)ca;
-  *reinterpret_cast<uint16_t*>(codes + r.b / 2) = (uint16_t)cb;
-  if (l == 0) (is_v ? c.v_pairs : c.k_pairs)[slot] = u.pair;
 }
 
 template <class DT, int D>
@@ -129,11 +164,11 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4CacheArg c, Kv4Ba
                                                             uint16_t* __restrict__ v_out) {
   constexpr int LPV = D / 8, VPB = kThreads / LPV;
   const int l = threadIdx.x % LPV;
-  const int64_t v = (int64_t)blockIdx.x * VPB + threadIdx.x / LPV;
+  const uint32_t v = blockIdx.x * VPB + threadIdx.x / LPV, heads = 2 * c.kv_heads;
   const int b = blockIdx.y;
   const Kv4Seq sq = kv4_seq(bt, b);
-  const int64_t i = v / (2 * c.kv_heads);
-  int h = (int)(v - i * 2 * c.kv_heads);
+  const int i = v / heads;
+  int h = v - i * heads;
   if (i >= sq.n) return;
   const bool is_v = h >= c.kv_heads;
   if (is_v) h -= c.kv_heads;

@@ -18,16 +18,22 @@ namespace qlora {
 // NaN too.
 
 // The largest bf16 value not above x, as fp32 bits.
-__device__ __forceinline__ uint32_t bf16_down(double x) {
-  const uint32_t b = __float_as_uint(__double2float_rd(x));
-  const uint32_t low = b & 0xFFFFu;
+__device__ __forceinline__ uint32_t bf16_down(float x) {
+  const uint32_t b = __float_as_uint(x), low = b & 0xFFFFu;
   return b - low + ((low && (b >> 31)) ? 0x10000u : 0u);
 }
-// The smallest bf16 value not below x, as fp32 bits.
-__device__ __forceinline__ uint32_t bf16_up(double x) {
-  const uint32_t b = __float_as_uint(__double2float_ru(x));
+__device__ __forceinline__ uint32_t bf16_down(double x) { return bf16_down(__double2float_rd(x)); }
+// (hi - m) / 15 rounded up to bf16, as fp32 bits.  The fp32 quotient is within
+// 2^-22 of the exact one, so it tells which bf16 values lie around it unless
+// its low 16 bits are next to 0; then the division is done in fp64.
+__device__ __forceinline__ uint32_t u4_step(double range) {
+  uint32_t b = __float_as_uint((float)range * (1.0f / 15.0f));
   const uint32_t low = b & 0xFFFFu;
-  return b - low + ((low && !(b >> 31)) ? 0x10000u : 0u);
+  if (low - 8u >= 0xFFF0u || b < 0x01000000u) {
+    b = __float_as_uint(__double2float_ru(range / 15.0));
+    return b - (b & 0xFFFFu) + ((b & 0xFFFFu) ? 0x10000u : 0u);
+  }
+  return b - low + 0x10000u;
 }
 
 struct U4Coder {
@@ -36,23 +42,25 @@ struct U4Coder {
   uint32_t pair;
 };
 
-// finite: every value of the group is finite
-__device__ __forceinline__ U4Coder u4_coder(double lo, double hi, bool finite) {
+// finite: every value of the group is finite.  T: the values' type, fp32 or
+// fp64.
+template <class T>
+__device__ __forceinline__ U4Coder u4_coder(T lo, T hi, bool finite) {
   U4Coder u;
   u.m = __uint_as_float(bf16_down(lo));
-  u.s = __uint_as_float(bf16_up((hi - (double)u.m) / 15.0));
+  u.s = __uint_as_float(u4_step((double)hi - (double)u.m));
   // also false for an infinite or NaN m or s
   finite = finite && fabsf(u.m) <= 3.4e38f && fabsf(u.s) <= 3.4e38f;
   if (!finite) u.s = u.m = __uint_as_float(0x7FC00000u);
   // below 2^-100 the fp32 reciprocal nears its range: take the exact path
-  u.inv = u.s > 0x1p-100f ? 1.0f / u.s : 0.0f;
+  u.inv = u.s > 0x1p-100f ? __builtin_amdgcn_rcpf(u.s) : 0.0f;
   u.pair = (__float_as_uint(u.s) >> 16) | (__float_as_uint(u.m) & 0xFFFF0000u);
   return u;
 }
 
 // rint((v - m) / s), t = fp32(v - m).  The fp32 quotient t * inv is within
-// 15 * 2^-22 (t, inv and the product are each rounded once) of the exact
-// one, so it decides the code wherever it lies further than 1e-4 from a
+// 15 * 2^-22 (t and the product are rounded once, inv is good to a unit in the
+// last place) of the exact one, so it decides the code wherever it lies further than 1e-4 from a
 // half; the few others (about one in 5000) divide in fp64.
 __device__ __forceinline__ uint32_t u4_code(const U4Coder& u, double v, float t) {
   const float q = t * u.inv;

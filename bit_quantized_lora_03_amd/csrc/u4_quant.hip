@@ -38,7 +38,7 @@ __global__ __launch_bounds__(kThreads) void quantize_u4_kernel(const float* __re
 #pragma unroll
     for (int i = 0; i < 4; ++i) fin = fin && fabsf(v[b][i]) <= 3.4028235e38f;
     lanes_minmax<LANES>(lo, hi);
-    const U4Coder u = u4_coder(lo, hi, lanes_all<LANES>(fin));
+    const U4Coder u = u4_coder<float>(lo, hi, lanes_all<LANES>(fin));
     uint32_t c = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) c |= u4_code(u, v[b][i], v[b][i] - u.m) << (4 * i);
