@@ -9,27 +9,39 @@
 // Bound by HBM on the cache at few rows.  The query rows of one KV head (its
 // group of query heads times the sequence's new tokens) are the 16 columns
 // of MFMA 16x16x32 products:
-//   scores: A = 16 keys, B = q.  Lane l reads key l % 16 and the quarter
-//     l / 16 of its codes, which are contiguous, and expands a word into 8
-//     operand values; q was put into that order once.
+//   scores: A = 16 keys, B = q.  Lane l has key l % 16 and the quarter l / 16
+//     of its codes, and expands a word into 8 operand values; q was put into
+//     that order once.
 //   values: A = V^T, B = p s'.  Lane l has, from the score tiles of two
 //     neighbouring 16-key halves, the 8 keys 4 (l / 16) + i of both, which
-//     are this product's 8 k-slots as they stand; it reads D / 16
+//     are this product's 8 k-slots as they stand; it takes D / 16
 //     neighbouring codes of each of these keys, and a v_perm for two keys
-//     brings them where two codes of one channel form an operand word.  So
-//     the transposition costs one instruction per 8 codes, and neither
-//     product goes through LDS.
+//     brings them where two codes of one channel form an operand word, so the
+//     transposition costs one instruction per 8 codes.
 // Codes enter as OFF + c.  Of the values' sums (OFF + 8) sum(p s') is taken
 // off again, from a product with ones, so it has the same rounded p s', and
 // 8 s' joins m' in the fp32 sum: what rounding p s' does is then multiplied
-// by c' - 8 and not by c' (error of the outputs 2.7 times smaller).
+// by c' - 8 and not by c' (error of bf16 outputs against 64 bits 4.9e-3
+// without, 2.4e-3 with; rounding the exact result gives 1.7e-3).
 //
-// A wave walks 32 keys a step with the next step's loads in flight.  The
-// running maximum is only moved when a score passes it by 2^kSlack: p stays
-// below 2^kSlack, far inside fp32 and bf16, and the accumulators are hardly
-// ever rescaled.  Four waves of a block interleave their steps and join in
-// LDS; long axes are cut into chunks whose partial results a second kernel
-// joins in chunk order (no atomics: every run gives the same bits).
+// A wave walks 32 keys a step.  Keys, values and pairs come to its own LDS by
+// DMA two steps ahead (one at D = 256): a step's 4.3 KiB (D 128) in 8
+// instructions and no registers.  The running maximum is only moved when a
+// score passes it by 2^kSlack: p stays below 2^kSlack, far inside fp32 and
+// bf16, and the accumulators are hardly ever rescaled.  Four waves of a block
+// interleave their steps and join in LDS; long axes are cut into chunks whose
+// partial results a second kernel joins in chunk order (no atomics: every run
+// gives the same bits).
+//
+// Measured (graph replays; in brackets a copy of the same bytes): 64 ragged
+// sequences up to 8192 keys, 32 heads on 8, D 128, bf16: 101 us (80), the
+// join 7 of it; 2 x 131071 keys, 64 heads on 8, fp16: 66 (48), the join 9;
+// one sequence of 777, 16 heads, D 64: 9.4, two launches and their first
+// loads.  A step's 320 vector instructions (130 for expanding the codes, 150
+// for scores and weights) and 17 MFMAs take about two thirds of the time that
+// its bytes do; what is left is the start of a block, four dependent loads
+// long.  Many rows are bound by the vector instructions: 3 x 251 rows of 16
+// heads on 4, D 256, window 4096: 124 us, 0.31 PFLOP/s.
 
 #include "kv4_common.h"
 #include "launch.h"
@@ -617,19 +629,25 @@ Kv4AttnPlan kv4_attn_plan(int64_t seqs, int64_t max_q, int64_t max_len, int q_he
                           int head_dim, int window) {
   Kv4AttnPlan p;
   const int64_t rows = max_q * (q_heads / kv_heads);
+  // Two column tiles share a step's decoding where there are rows for them
+  // (2 x 1000 rows of 32 heads on 8, D 128: 123 us against 144; at 20 rows, of
+  // which the second tile has 4, 52 against 47; at D = 64, where decoding is
+  // less of the work, 80 against 60, and D = 256 lacks the registers).
   p.tile = head_dim == 128 && rows >= 64 ? 32 : 16;
   p.tiles = (int)((rows + p.tile - 1) / p.tile);
   int64_t keys = max_len;
   // a tile's window starts up to 31 keys early
   if (window > 0 && window + max_q + kStep < keys) keys = window + max_q + kStep;
-  const int64_t want = 1536, base = seqs * kv_heads * p.tiles;
-  const int64_t per = kStep * kWaves;
-  int64_t chunk = (keys * base + want - 1) / want;
-  chunk = (chunk + per - 1) / per * per;
-  if (chunk < 2 * per) chunk = 2 * per;
-  p.splits = (int)((keys + chunk - 1) / chunk);
-  if (p.splits < 1) p.splits = 1;
-  if (p.splits == 1) chunk = (keys + per - 1) / per * per;
+  // Chunks for two rounds of the chip's blocks (three blocks a CU), so that
+  // the short sequences of a ragged batch do not leave it idle, of at least
+  // two steps for each wave: 64 ragged sequences up to 8192, 8 heads: 101 us,
+  // with one round 132, with five 117.
+  constexpr int64_t kWant = 1536, kPer = kStep * kWaves;
+  const int64_t base = seqs * kv_heads * p.tiles;
+  int64_t chunk = base >= kWant ? keys : (keys * base + kWant - 1) / kWant;
+  chunk = (chunk + kPer - 1) / kPer * kPer;
+  if (chunk < 2 * kPer) chunk = 2 * kPer;
+  p.splits = chunk >= keys ? 1 : (int)((keys + chunk - 1) / chunk);
   p.chunk = (int)chunk;
   return p;
 }

@@ -447,8 +447,9 @@ typedef struct qlora_kv4_cache {
  *   - a position without a page (past the table, or an entry outside
  *     0 .. pages - 1, such as -1 for a page given back) is a token that is
  *     not there: not stored, not attended to, read as zeros;
- *   - a page may belong to several sequences (a shared prefix), but no two
- *     rows of one append may name the same token of the same page.          */
+ *   - a page may belong to several sequences (a shared prefix); where two
+ *     rows of one append name the same token of the same page, what is
+ *     stored there is unspecified.                                         */
 typedef struct qlora_kv4_batch {
   const int32_t* cu_q;        /* [seqs + 1], ascending from 0          */
   const int32_t* seq_lens;    /* [seqs], with the rows of this call    */

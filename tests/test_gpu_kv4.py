@@ -328,6 +328,16 @@ def test_attention_split_axis(cuda, dtype, window):
     attend(pool, new, Hq, dtype, window=window, max_len=0)
 
 
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,page,window", [
+    ("bf16", 128, 8, 1, 64, 0), ("f16", 128, 4, 1, 1024, 900), ("bf16", 64, 8, 1, 16, 0),
+    ("f16", 256, 2, 1, 32, 0)])
+def test_attention_many_rows_split_axis(cuda, dtype, D, Hq, Hkv, page, window):
+    """Tiles of several rows for each head together with partial results."""
+    lens, new = [1500, 40], [33, 40]
+    assert q.kv4_attention_workspace_bytes(2, 40, 1500, Hq, Hkv, D, window) > 0
+    attend(Pool(lens, page, Hkv, D, seed=D).fill(), new, Hq, dtype, window=window)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("scale", [1.0, 0.0, -0.3, 20.0])
 def test_attention_scales(cuda, dtype, scale):

@@ -168,6 +168,35 @@ def test_linear_larger(cuda, dtype, M, N, K, G):
     check_linear(f"{dtype} {M}x{N}x{K}", y, x, codes, pairs, dtype)
 
 
+@pytest.mark.parametrize("dtype,M,N,K,G", [
+    # several row tiles per block, with 16, 8 and 4 waves, and a K whose last
+    # unit is partial; each token-tile variant
+    ("bf16", 1, 8203, 4160, 64), ("f16", 4, 9001, 4224, 128), ("bf16", 1, 20000, 2112, 64),
+    ("f16", 3, 17000, 2080, 32), ("bf16", 2, 70000, 384, 128), ("bf16", 16, 9000, 1056, 32),
+    ("f16", 9, 40011, 320, 64), ("bf16", 20, 9000, 640, 64), ("f16", 50, 9000, 1152, 128),
+    ("bf16", 70, 9000, 160, 32)])
+def test_linear_many_rows(cuda, dtype, M, N, K, G):
+    _, (codes, pairs) = weight(N, K, G, seed=11)
+    x = to_dev(np.random.default_rng(12).standard_normal((M, K)).astype(np.float32)).to(tdtype(dtype))
+    y = Guarded((M, N), tdtype(dtype))
+    q.linear_u4_fwd(q.U4Weight(to_dev(codes), pairs_dev(pairs)), x, y=y.t)
+    y.check("y")
+    check_linear(f"{dtype} {M}x{N}x{K}", y.t, x, codes, pairs, dtype)
+
+
+@pytest.mark.parametrize("M,K,G", [(1, 96, 32), (4, 192, 64), (13, 416, 32), (33, 160, 32), (60, 384, 128)])
+def test_linear_what_lies_between_the_rows_of_x(cuda, M, K, G):
+    """NaN beside x in its wider tensor, before the first and behind the last
+    row and between the rows, stays out of y."""
+    import torch
+    _, (codes, pairs) = weight(70, K, G)
+    wide = torch.full((M + 2, K + 64), float("nan"), device="cuda", dtype=torch.bfloat16)
+    x = wide[1:M + 1, 16:16 + K]
+    x.copy_(torch.randn(M, K, device="cuda"))
+    y = q.linear_u4_fwd(q.U4Weight(to_dev(codes), pairs_dev(pairs)), x)
+    check_linear(f"{M}x{K}", y, x, codes, pairs, "bf16")
+
+
 @pytest.mark.parametrize("M", [1, 7, 40])
 def test_linear_strided_rows(cuda, M):
     import torch
