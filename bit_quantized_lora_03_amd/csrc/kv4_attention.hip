@@ -274,8 +274,7 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
                          U4Mfma<Bf16T>::kOne};
   const TablePtr table = (TablePtr)(bt.block_table + (int64_t)b * bt.table_width);
 
-  // one step; the next one's keys are asked for once these are used, and its
-  // values likewise, so one set of registers serves both
+  // one step on the stage at s; have: which of its halves have a page
   auto step = [&](const uint8_t* s, uint32_t have, int t) __attribute__((always_inline)) {
     // some row of the tile does not see some key of the step
     const bool masked = have != 3 || t < all_lo || t + kStep > all_hi;
