@@ -30,8 +30,8 @@
 // bytes): M 1, 4096 x 4096, groups of 64: 4.8 us (2.0); M 1, 8192 x 8192:
 // 10.5 (7.9); M 4, 22016 x 8192: 25 (21.3); M 16, 8192 x 8192: 14.4 (7.6),
 // where x, 256 KiB for each block, is twice the codes' traffic into the CUs;
-// M 61, 11008 x 4096, groups of 32: 28 (6.3), bound by the vector
-// instructions that scale the sums (8 for each group and token tile).
+// M 61, 11008 x 4096, groups of 32: 25 (6.3), bound by the vector
+// instructions that decode the codes and scale the sums.
 
 #include "launch.h"
 #include "u4_common.h"
@@ -189,15 +189,37 @@ __global__ __launch_bounds__(64 * W) void linear_u4_kernel(
         for (int t = 0; t < NT; ++t)
           d[g][t] = DT::mfma16(xo[g * C + c][t], b, c ? d[g][t] : f32x4_t{0, 0, 0, 0});
       }
+    // (m - OFF s) X: where a unit has four groups or more and there are more
+    // tokens than 16, as an fp32 product whose k-slots are four groups (lane:
+    // group 4 e + l / 16), for the vector instructions bound the kernel there
+    // (N 11008, K 4096, groups of 32: M 61 28.0 us without, 24.9 with; M 32
+    // 23.0 and 20.0).  With fewer groups slots are empty and it is slower (M 61,
+    // groups of 128: 20.8 us without, 21.9 with).
+    constexpr bool kSlots = NT > 1 && S::kPairs >= 4;
+    if constexpr (kSlots) {
+#pragma unroll
+      for (int e = 0; e < S::kPairs / 4; ++e) {
+        const int g = 4 * e + lg;
+        const bool valid = all || u * S::kPairs + g < groups;
+        const uint32_t w = st.w.p[lr][g];
+        const float m = valid ? fmaf(-U4Mfma<DT>::kOff, u4_s(w), u4_m(w)) : 0.0f;
+        const float* X = reinterpret_cast<const float*>(st.X[g]) + lr;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          a[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(valid ? X[16 * t] : 0.0f, m, a[t], 0, 0, 0);
+      }
+    }
 #pragma unroll
     for (int g = 0; g < S::kPairs; ++g) {
       if (!all && u * S::kPairs + g >= groups) break;
       const float s = u4_s(pair[g]), m = fmaf(-U4Mfma<DT>::kOff, s, u4_m(pair[g]));
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const f32x4_t X = st.X[g][4 * t + lg];
+        f32x4_t X = {0, 0, 0, 0};
+        if constexpr (!kSlots) X = st.X[g][4 * t + lg];
 #pragma unroll
-        for (int i = 0; i < TI; ++i) a[t][i] = fmaf(s, d[g][t][i], fmaf(m, X[i], a[t][i]));
+        for (int i = 0; i < TI; ++i)
+          a[t][i] = fmaf(s, d[g][t][i], kSlots ? a[t][i] : fmaf(m, X[i], a[t][i]));
       }
     }
 #pragma unroll
@@ -244,9 +266,10 @@ __global__ __launch_bounds__(64 * W) void linear_u4_kernel(
   }
 }
 
-template <class DT, int G, int NT, int XQ, int TI, int W>
+template <class DT, int G, int NT, int XQ, int TI, int W, int CAP>
 void go(const uint8_t* codes, const uint32_t* pairs, const uint16_t* x, int64_t ldx, uint16_t* y,
         int64_t ldy, int64_t M, int64_t N, int64_t K, int R, hipStream_t s) {
+  static_assert(W * (sizeof(Stage<G, NT>) + CAP * NT * 1024) <= 160 * 1024, "LDS of a CU");
   const dim3 grid((unsigned)((N + 16 * R - 1) / (16 * R)), (unsigned)((M + 16 * NT - 1) / (16 * NT)));
   linear_u4_kernel<DT, G, NT, XQ, TI, W><<<grid, 64 * W, (size_t)W * R * NT * 1024, s>>>(
       codes, pairs, x, ldx, y, ldy, M, N, K, R);
@@ -264,8 +287,8 @@ template <class DT, int G>
 void pick(const uint8_t* codes, const uint32_t* pairs, const uint16_t* x, int64_t ldx, uint16_t* y,
           int64_t ldy, int64_t M, int64_t N, int64_t K, hipStream_t s) {
 #define QLORA_U4_GO(NT, XQ, TI, W, CAP, PER_CU)                                              \
-  return go<DT, G, NT, XQ, TI, W>(codes, pairs, x, ldx, y, ldy, M, N, K,                  \
-                                     tiles_per_block(N, 256 * (PER_CU), CAP), s)
+  return go<DT, G, NT, XQ, TI, W, CAP>(codes, pairs, x, ldx, y, ldy, M, N, K,             \
+                                       tiles_per_block(N, 256 * (PER_CU), CAP), s)
   const int64_t units = (K + 255) / 256;
   if (M <= 4) {
     // 16 waves a block (one block per CU) where each still has a unit and
