@@ -436,9 +436,13 @@ const char* qlora_status_string(int status) {
     case QLORA_EINVAL: return "invalid argument (null pointer, negative size or aliasing)";
     case QLORA_ESHAPE:
       return "unsupported shape (N, K must be multiples of 64; r a multiple of 8 <= 256; "
-             "codes, each activation tensor, A, B and the adapter products below 2 GiB)";
-    case QLORA_EALIGN: return "device pointer not 16-byte aligned";
-    case QLORA_ENOTSUP: return "unsupported block size (64 / 256 only)";
+             "codes, each activation tensor, A, B and the adapter products below 2 GiB; "
+             "the 4-bit serving calls: a length, head layout or stride outside their limits)";
+    case QLORA_EALIGN:
+      return "device pointer or stride not aligned as declared (most: 16 bytes)";
+    case QLORA_ENOTSUP:
+      return "unsupported block size (64 / 256 only), 4-bit group (32 / 64 / 128), cache page "
+             "(a power of two, 16 to 1024) or head size (64 / 128 / 256)";
     case QLORA_EWORKSPACE: return "workspace missing or too small";
     case QLORA_EHIP: return "HIP launch or runtime error";
     case QLORA_ESCRATCH:

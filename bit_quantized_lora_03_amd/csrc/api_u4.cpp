@@ -16,6 +16,12 @@ constexpr int64_t kMaxRows = int64_t{1} << 30;
 // The product's kernel reads 128 rows of codes and 64 of x with 32-bit offsets.
 constexpr int64_t kMaxK = int64_t{1} << 23;
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
+// A launch holds below 2^32 threads along x.  Of a product they are at most
+// 512 for 3 tiles of 16 rows; of a head vector a lane for 8 values; of the
+// attention 256 for a tile of 16 query rows.
+constexpr int64_t kMaxN = int64_t{1} << 28;
+constexpr int64_t kMaxVectorValues = int64_t{1} << 34;
+constexpr int64_t kMaxQueryRows = int64_t{1} << 27;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -53,7 +59,7 @@ int check_u4(const qlora_u4_weight* w) {
   if (!w || !w->codes || !w->pairs) return QLORA_EINVAL;
   if (w->N <= 0 || w->K <= 0) return QLORA_EINVAL;
   if (!group_ok(w->group)) return QLORA_ENOTSUP;
-  if (w->K % w->group || w->K > kMaxK || w->N >= kMaxRows) return QLORA_ESHAPE;
+  if (w->K % w->group || w->K > kMaxK || w->N >= kMaxN) return QLORA_ESHAPE;
   if (!aligned(w->codes, 16) || !aligned(w->pairs, 16)) return QLORA_EALIGN;
   return QLORA_OK;
 }
@@ -175,7 +181,8 @@ int append(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, const uin
       if (!q_out) return QLORA_EINVAL;
       if (!aligned(q_out, 16)) return QLORA_EALIGN;
     }
-    if ((int64_t)b.max_q * (q_heads + 2 * c.kv_heads) > kMaxGrid) return QLORA_ESHAPE;
+    if ((int64_t)b.max_q * (q_heads + 2 * c.kv_heads) > kMaxVectorValues / c.head_dim)
+      return QLORA_ESHAPE;
     const size_t cb = code_bytes(cache), pb = pair_bytes(cache);
     if (clash<5, 7>({{c.k_codes, cb},
                      {c.v_codes, cb},
@@ -209,7 +216,7 @@ int read(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, uint16_t* k
     if (no_rows(batch)) return QLORA_OK;
     if (!k_out || !v_out) return QLORA_EINVAL;
     if (!aligned(k_out, 16) || !aligned(v_out, 16)) return QLORA_EALIGN;
-    if ((int64_t)b.max_q * 2 * c.kv_heads > kMaxGrid) return QLORA_ESHAPE;
+    if ((int64_t)b.max_q * 2 * c.kv_heads > kMaxVectorValues / c.head_dim) return QLORA_ESHAPE;
     const size_t cb = code_bytes(cache), pb = pair_bytes(cache),
                  no = (size_t)b.rows * c.kv_heads * c.head_dim * 2;
     if (clash<2, 7>({{k_out, no}, {v_out, no}},
@@ -236,7 +243,7 @@ int attn_plan(int64_t seqs, int64_t max_q, int64_t max_len, int32_t q_heads, int
   if (seqs > 65535 || max_q > kMaxRows || max_len > kMaxRows || kv_heads > 4096 ||
       q_heads > 65536 || q_heads % kv_heads)
     return QLORA_ESHAPE;
-  if (max_q * (q_heads / kv_heads) > kMaxRows) return QLORA_ESHAPE;
+  if (max_q * (q_heads / kv_heads) > kMaxQueryRows) return QLORA_ESHAPE;
   *p = qlora::kv4_attn_plan(seqs, max_q, max_len, q_heads, kv_heads, head_dim, window);
   return QLORA_OK;
 }
@@ -282,8 +289,8 @@ int attention(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, const 
     const qlora::Kv4AttnArg a{q,      q_ts,   q_hs, q_heads,
                               scale,  causal, window,
                               (int64_t)b.table_width * cache->page_size, out, lse};
-    return hip_status(qlora::launch_kv4_attention(c, b, a, p, need > 0 ? static_cast<float*>(workspace) : nullptr,
-                                                  f16, as_stream(stream)));
+    float* ws = need > 0 ? static_cast<float*>(workspace) : nullptr;
+    return hip_status(qlora::launch_kv4_attention(c, b, a, p, ws, f16, as_stream(stream)));
   } catch (...) {
     return QLORA_EHIP;
   }

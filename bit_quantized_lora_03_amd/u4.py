@@ -189,8 +189,8 @@ def _batch(cache: Kv4Cache, cu_q, seq_lens, block_table, max_q: int, rows: int) 
     cs, ls, bs = cu_q.shape, seq_lens.shape, block_table.shape
     if len(ls) != 1 or len(cs) != 1 or len(bs) != 2 or cs[0] != ls[0] + 1 or bs[0] != ls[0]:
         raise ValueError("cu_q [B + 1], seq_lens [B] and block_table [B, width] are needed")
-    if max_q < 0:
-        raise ValueError("max_q is negative")
+    if not 0 <= max_q < 2 ** 31:
+        raise ValueError(f"max_q {max_q} is out of range")
     return Kv4BatchStruct(cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), rows,
                           ls[0], bs[1], max_q)
 
@@ -270,6 +270,8 @@ def kv4_read(cache: Kv4Cache, cu_q, seq_lens, block_table, max_q: int, rows: int
 
 def kv4_attention_workspace_bytes(seqs: int, max_q: int, max_len: int, q_heads: int,
                                   kv_heads: int, head_dim: int, window: int = 0) -> int:
+    if not -2 ** 31 <= window < 2 ** 31:  # a negative one is the library's to refuse
+        raise ValueError(f"window {window} is out of range")
     return int(_lib.lib().qlora_kv4_attention_workspace_bytes(seqs, max_q, max_len, q_heads,
                                                               kv_heads, head_dim, window))
 
@@ -298,6 +300,8 @@ def kv4_attention(cache: Kv4Cache, q, cu_q, seq_lens, block_table, max_q: int, m
               and lse.get_device() == index, f"lse: fp32 [{T}, {heads}] is needed")
     elif return_lse:
         lse = torch.empty((T, heads), dtype=_f32, device=device)
+    if not -2 ** 31 <= window < 2 ** 31:  # a negative one is the library's to refuse
+        raise ValueError(f"window {window} is out of range")
     need = _lib.lib().qlora_kv4_attention_workspace_bytes(bt.seqs, max_q, max_len, heads,
                                                           cache.kv_heads, D, window)
     if workspace is None:

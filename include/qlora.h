@@ -55,9 +55,11 @@ extern "C" {
 #define QLORA_OK          0
 #define QLORA_EINVAL     (-1) /* null pointer, negative size, aliasing        */
 #define QLORA_ESHAPE     (-2) /* K or N not a multiple of 64, r > 256 or r%8,
-                                  or a tensor at or above 2 GiB (see below)    */
+                                  or a tensor at or above 2 GiB (see below);
+                                  4-bit serving: as said at each call          */
 #define QLORA_EALIGN     (-3) /* a device pointer is not 16-byte aligned      */
-#define QLORA_ENOTSUP    (-4) /* blocksize != 64 or blocksize2 != 256         */
+#define QLORA_ENOTSUP    (-4) /* blocksize != 64 or blocksize2 != 256; 4-bit
+                                  serving: group, page or head size            */
 #define QLORA_EWORKSPACE (-5) /* workspace NULL or smaller than required      */
 #define QLORA_EHIP       (-6) /* a HIP launch or runtime call failed          */
 #define QLORA_ESCRATCH   (-7) /* the allocation-free call needs more than
@@ -389,11 +391,13 @@ int qlora_linear_fwd_noalloc(const qlora_nf4_weight* w, const uint16_t* x, int64
  *   range, gets m = s = NaN and codes 0, and so decodes to NaN.  (These
  *   calls take such inputs; those above do not check for them.)
  * A weight [N, K] has groups of 32, 64 or 128 along K (4 + 32 / group bits
- * per weight).  Device pointers, 16-byte aligned unless said otherwise.     */
+ * per weight).  Device pointers, 16-byte aligned unless said otherwise.  No
+ * output may overlap an input or another output (EINVAL); of strided tensors
+ * that is the range from the first to the last element, gaps included.      */
 typedef struct qlora_u4_weight {
   const uint8_t*  codes;  /* [N, K/2]            */
   const uint16_t* pairs;  /* [N, K/group, 2]     */
-  int64_t         N;      /* 1 .. 2^30 - 1       */
+  int64_t         N;      /* 1 .. 2^28 - 1       */
   int64_t         K;      /* a multiple of group, up to 2^23 (ESHAPE) */
   int32_t         group;  /* 32, 64 or 128 (ENOTSUP)                  */
 } qlora_u4_weight;
@@ -457,7 +461,9 @@ typedef struct qlora_kv4_batch {
   int64_t        rows;        /* rows of the row tensors, up to 2^30   */
   int32_t        seqs;        /* up to 65535 (ESHAPE)                  */
   int32_t        table_width; /* table_width * page_size up to 2^30    */
-  int32_t        max_q;       /* at least the most rows of a sequence  */
+  int32_t        max_q;       /* at least the most rows of a sequence;
+                                 times heads * head_dim up to 2^34, times
+                                 q_heads / kv_heads up to 2^27 (ESHAPE) */
 } qlora_kv4_batch;
 
 /* Append the batch's keys and values to the cache, rotated by position.
@@ -513,7 +519,8 @@ int qlora_kv4_read_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch* batc
  * scale must be finite (EINVAL).  workspace (256-byte aligned): at least
  * qlora_kv4_attention_workspace_bytes(seqs, max_q, max_len, ...) bytes, or
  * NULL where that is 0 (also its answer for an invalid shape); it is written
- * before it is read.  Host-only; the same bits on every run of a shape.     */
+ * before it is read (the workspace's size is worked out on the host).  The
+ * same bits on every run of a shape.                                        */
 size_t qlora_kv4_attention_workspace_bytes(int64_t seqs, int64_t max_q, int64_t max_len,
                                            int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                            int32_t window);

@@ -473,6 +473,18 @@ def test_python_refusals(cuda):
         q.kv4_attention(c, qq, cu, lens, table, 1, 1 << 18, workspace=ws)
 
 
+def test_sizes_past_32_bits_do_not_wrap(cuda):
+    import torch
+    pool = Pool([20], 16, 2, 64).fill()
+    c, (cu, lens, table) = pool.cache(), pool.ints([1])
+    k = torch.zeros(1, 2, 64, device="cuda", dtype=torch.bfloat16)
+    qq = torch.zeros(1, 4, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        q.kv4_append(c, k, k, cu, lens, table, (1 << 32) + 1)
+    with pytest.raises(ValueError):
+        q.kv4_attention(c, qq, cu, lens, table, 1, 20, window=(1 << 32) + 1)
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------

@@ -236,3 +236,24 @@ def test_importing_the_package_does_without_torch():
             "q.linear_u4_fwd; assert 'torch' in sys.modules")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     assert subprocess.run([sys.executable, "-c", code], cwd=root).returncode == 0
+
+
+@pytest.mark.parametrize("tail", ["", "_f16"])
+def test_sizes_past_a_launch(tail):
+    """A launch has fewer than 2^32 threads along x; more is refused."""
+    L = q.lib()
+    big = weight(N=1 << 28, K=32, group=32, codes=1 << 40, pairs=1 << 42)
+    assert getattr(L, "qlora_linear_u4_fwd" + tail)(big, at(3), 32, 1, 1 << 44, 1 << 28,
+                                                    None) == ESHAPE
+    # 2^34 values of a sequence's head vectors: heads 4 + 2 x 2 of 64
+    b = batch(max_q=(1 << 25) + 1)
+    assert call_append(cache(), b, tail) == ESHAPE
+    assert call_read(cache(), batch(max_q=(1 << 26) + 1), tail) == ESHAPE
+    # 2^27 query rows of a KV head
+    b = batch(max_q=(1 << 26) + 1)
+    assert call_attention(cache(), b, tail) == ESHAPE
+
+
+def test_windows_past_32_bits_do_not_wrap():
+    with pytest.raises(ValueError):
+        q.kv4_attention_workspace_bytes(1, 1, 1 << 17, 8, 8, 64, (1 << 32) + 10)
