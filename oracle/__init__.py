@@ -24,6 +24,9 @@ What it computes (numpy, fp64 unless a step fixes another precision):
 * ``merge`` -- the adapter merged into a base weight for export,
   W_m = W_base + (alpha/r).B.A (fp32 and bf16 exports, re-quantisation, and
   the errors of the three ways to export).
+* ``u4``    -- the 4-bit group format, the product with such a weight, the
+  rotated append to the paged cache, reading it back and the attention over
+  it.
 
 Sources are cited by page title and section.  The pages state the format in
 words only; every reading taken where they are silent is written at the
