@@ -206,7 +206,12 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lg = lane >> 4;
   const int b = blockIdx.z, head = blockIdx.y;
-  const int tile = blockIdx.x / splits, split = blockIdx.x - tile * splits;
+  // Neighbouring blocks go to the eight XCDs in turn, and late chunks have less
+  // to do or nothing; so which block has which chunk turns from one tile, head
+  // and sequence to the next.  (Two chunks: 4 x 251 rows, window 4096, D 256:
+  // 147 us, 192 without; six: 48 ragged sequences up to 8000 keys, 71 and 81.)
+  const int tile = blockIdx.x / splits;
+  const int split = (blockIdx.x + tile + head + b) % splits;
   const int group = a.q_heads / c.kv_heads;
   const Kv4Seq sq = kv4_seq(bt, b);
   const int r0 = tile * (16 * NT), rows = (int)(sq.n * group);
