@@ -41,7 +41,9 @@
 // for scores and weights) and 17 MFMAs take about two thirds of the time that
 // its bytes do; what is left is the start of a block, four dependent loads
 // long.  Many rows are bound by the vector instructions: 3 x 251 rows of 16
-// heads on 4, D 256, window 4096: 124 us, 0.31 PFLOP/s.
+// heads on 4, D 256, window 4096: 106 us, 0.36 PFLOP/s.
+
+#include <algorithm>
 
 #include "kv4_common.h"
 #include "launch.h"
@@ -208,8 +210,9 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
   const int b = blockIdx.z, head = blockIdx.y;
   // Neighbouring blocks go to the eight XCDs in turn, and late chunks have less
   // to do or nothing; so which block has which chunk turns from one tile, head
-  // and sequence to the next.  (Two chunks: 4 x 251 rows, window 4096, D 256:
-  // 147 us, 192 without; six: 48 ragged sequences up to 8000 keys, 71 and 81.)
+  // and sequence to the next.  (With an even number of chunks: 48 ragged
+  // sequences up to 8000 keys, four chunks: 71 us, 81 without; 4 x 251 rows of
+  // D 256 in two: 147 and 192.)
   const int tile = blockIdx.x / splits;
   const int split = (blockIdx.x + tile + head + b) % splits;
   const int group = a.q_heads / c.kv_heads;
@@ -645,10 +648,17 @@ Kv4AttnPlan kv4_attn_plan(int64_t seqs, int64_t max_q, int64_t max_len, int q_he
   // Chunks for two rounds of the chip's blocks (three blocks a CU), so that
   // the short sequences of a ragged batch do not leave it idle, of at least
   // two steps for each wave: 64 ragged sequences up to 8192, 8 heads: 101 us,
-  // with one round 132, with five 117.
-  constexpr int64_t kWant = 1536, kPer = kStep * kWaves;
-  const int64_t base = seqs * kv_heads * p.tiles;
-  int64_t chunk = base >= kWant ? keys : (keys * base + kWant - 1) / kWant;
+  // with one round 109, with five 117.  Full tiles of rows, whose partial
+  // results are more of the work, for one round: 3 x 251 rows, window 4096, D
+  // 256: 106 us with one chunk, 126 with two; 700 rows on 8000 keys, D 128:
+  // 200 and 207.  Their number is rounded to the nearest: a last chunk of few
+  // keys costs all the partial results (3 x 500 rows, 1512 blocks: 205 us with
+  // a second chunk, 126 without).
+  const int64_t want = rows >= 64 ? 768 : 1536;
+  constexpr int64_t kPer = kStep * kWaves;
+  const int64_t base = std::max<int64_t>(seqs * kv_heads * p.tiles, 1);
+  const int64_t n = std::max<int64_t>((want + base / 2) / base, 1);
+  int64_t chunk = (keys + n - 1) / n;
   chunk = (chunk + kPer - 1) / kPer * kPer;
   if (chunk < 2 * kPer) chunk = 2 * kPer;
   p.splits = chunk >= keys ? 1 : (int)((keys + chunk - 1) / chunk);
