@@ -21,14 +21,20 @@
 // Codes enter as OFF + c.  Of the values' sums (OFF + 8) sum(p s') is taken
 // off again, from a product with ones, so it has the same rounded p s', and
 // 8 s' joins m' in the fp32 sum: what rounding p s' does is then multiplied
-// by c' - 8 and not by c' (error of bf16 outputs against 64 bits 4.9e-3
-// without, 2.4e-3 with; rounding the exact result gives 1.7e-3).
+// by c' - 8 and not by c'.
+// p s' is an fp16 operand (half a step is 2^-11): as a bf16 one (2^-8) it took
+// bf16 outputs 2.4e-3 from the 64-bit result; now they are 1.7e-3 off, as the
+// exact result rounded is (64 ragged sequences 101 us with either, many rows 3
+// to 4 % slower).  fp16 outputs take a second operand for what the first loses
+// (2^-22).  fp16's range is narrow, so the exponent that p is counted from
+// holds the largest s' of the row so far beside the largest score (kUp,
+// kLeastStep below).
 //
 // A wave walks 32 keys a step.  Keys, values and pairs come to its own LDS by
 // DMA two steps ahead (one at D = 256): a step's 4.3 KiB (D 128) in 8
 // instructions and no registers.  The running maximum is only moved when a
-// score passes it by 2^kSlack: p stays below 2^kSlack, far inside fp32 and
-// bf16, and the accumulators are hardly ever rescaled.  Four waves of a block
+// score passes it by 2^kSlack, and the largest s' goes up by powers of two, so
+// the accumulators are hardly ever rescaled.  Four waves of a block
 // interleave their steps and join in LDS; long axes are cut into chunks whose
 // partial results a second kernel joins in chunk order (no atomics: every run
 // gives the same bits).
@@ -55,6 +61,13 @@ constexpr int kWaves = 4;
 constexpr int kStep = 32;
 constexpr float kSlack = 8.0f;
 constexpr float kMid = 8.0f;
+// With E the power of two at or above the row's largest s' (at least
+// kLeastStep), p is counted as 2^(z log2 e - M + kUp) / E: p s' then is at most
+// 2^(kSlack + kUp) = 2^14, inside fp16, and 2^kUp at the running maximum, 2^20
+// above the smallest normal fp16.  (p itself, and sums of p, pass fp32's range
+// only where steps pass 2^100, or where all are below 2^-60.)
+constexpr float kUp = 6.0f;
+constexpr float kLeastStep = 0x1p-60f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -184,6 +197,14 @@ __device__ __forceinline__ float column_max(float v) {
   return fmaxf(v, __shfl_xor(v, 32));
 }
 
+// ln(2^m sum); the sum's exponent is added to m as it is, so that what p was
+// counted from costs no bits.
+__device__ __forceinline__ float log_sum(float m, float sum) {
+  int e;
+  const float f = frexpf(sum, &e);
+  return (m + (float)e + log2f(f)) * kLn2;
+}
+
 template <class DT, int D, int NT>
 __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attention_kernel(
     Kv4CacheArg c, Kv4BatchArg bt, Kv4AttnArg a, int chunk, int splits, int tiles,
@@ -191,10 +212,10 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
   constexpr int KC = D / 32;  // score products per half
   constexpr int VC = D / 16;  // value products, and codes per lane and key
   constexpr int VW = D == 64 ? 1 : D / 128;  // words of these
-  // fp16 keeps what p s' loses in bf16 (whose range it needs) as a second
-  // operand; bf16 results are rounded to the operand's precision anyway
+  // what an fp16 operand loses of p s' is a second one for fp16 results; bf16
+  // results are rounded to an eighth of its precision
   constexpr bool kSplitP = std::is_same_v<DT, F16T>;
-  constexpr float kOffK = U4Score<DT>::kOff, kOffV = U4Mfma<Bf16T>::kOff + kMid;
+  constexpr float kOffK = U4Score<DT>::kOff, kOffV = U4Value::kOff + kMid;
   constexpr int OS = D + 4;
   using R = Ring<D>;
   // the rings, and after the walk the place of the waves' sums
@@ -254,14 +275,15 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
   const int all_hi = (int)max(a.causal ? min(sq.len, sq.pos0 + sp.i0 + 1) : sq.len, (int64_t)0);
 
   f32x4_t o[NT][VC], po[NT];
-  float m[NT], mu[NT], l[NT], cs[NT];
+  float m[NT], mu[NT], l[NT], cs[NT], big[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int j = 0; j < VC; ++j) o[n][j] = f32x4_t{0, 0, 0, 0};
     po[n] = f32x4_t{0, 0, 0, 0};
     m[n] = -INFINITY;  // running maximum of the products q.k
-    mu[n] = 0.0f;      // the same in log2 units, 0 while it is -inf
+    mu[n] = 0.0f;      // what p is counted from, in log2 units; 0 while m is -inf
+    big[n] = kLeastStep;  // the power of two at or above every s' so far
     l[n] = cs[n] = 0.0f;
   }
   // never 0, which would make a hidden score, -inf, NaN; 2^-100 is as good
@@ -278,8 +300,7 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     voff[i] = R::kCodes + R::place(4 * lg + i, lr * (D / 32) / 16) + lr * (D / 32) % 16;
-  const u32x4_t onesv = {U4Mfma<Bf16T>::kOne, U4Mfma<Bf16T>::kOne, U4Mfma<Bf16T>::kOne,
-                         U4Mfma<Bf16T>::kOne};
+  const u32x4_t onesv = {U4Value::kOne, U4Value::kOne, U4Value::kOne, U4Value::kOne};
   const TablePtr table = (TablePtr)(bt.block_table + (int64_t)b * bt.table_width);
 
   // one step on the stage at s; have: which of its halves have a page
@@ -338,11 +359,24 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
       }
       float top = fmaxf(fmaxf(fmaxf(z[n][0][0], z[n][0][1]), fmaxf(z[n][0][2], z[n][0][3])),
                         fmaxf(fmaxf(z[n][1][0], z[n][1][1]), fmaxf(z[n][1][2], z[n][1][3])));
-      if (__any(top > m[n] + slack)) {
+      float vs[2][4], most = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vs[h][i] = u4_s(vp[h][i]);
+          most = fmaxf(most, fabsf(vs[h][i]));
+        }
+      if (__any(top > m[n] + slack || most > big[n])) {
         top = fmaxf(column_max(top), m[n]);
         const float was = m[n] == -INFINITY ? -INFINITY : mu[n];
         m[n] = top;
-        mu[n] = top == -INFINITY ? 0.0f : top * c1;
+        // the power of two above `most`; NaN and infinities leave it, whose sums
+        // are not finite anyway
+        const uint32_t e = __float_as_uint(column_max(most)) & 0x7F800000u;
+        big[n] = fmaxf(big[n], e < 0x7F000000u ? __uint_as_float(e + 0x00800000u) : 0x1p127f);
+        const int up = (int)(__float_as_uint(big[n]) >> 23) - 127;
+        mu[n] = top == -INFINITY ? 0.0f : fmaf(top, c1, (float)up - kUp);
         const float f = __builtin_amdgcn_exp2f(was - mu[n]);
 #pragma unroll
         for (int j = 0; j < VC; ++j)
@@ -359,21 +393,20 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float p = __builtin_amdgcn_exp2f(fmaf(z[n][h][i], c1, -mu[n]));
-          const float vs = u4_s(vp[h][i]);
           l[n] += p;
-          ps[h][i] = p * vs;
-          cs[n] = fmaf(p, fmaf(kMid, vs, u4_m(vp[h][i])), cs[n]);
+          ps[h][i] = p * vs[h][i];
+          cs[n] = fmaf(p, fmaf(kMid, vs[h][i], u4_m(vp[h][i])), cs[n]);
         }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float u0 = ps[w >> 1][2 * (w & 1)], u1 = ps[w >> 1][2 * (w & 1) + 1];
-        pb[n][w] = Bf16T::pack2(u0, u1);
+        pb[n][w] = F16T::pack2(u0, u1);
         if constexpr (kSplitP)
-          pl[n][w] = Bf16T::pack2(u0 - __uint_as_float(pb[n][w] << 16),
-                                  u1 - __uint_as_float(pb[n][w] & 0xFFFF0000u));
+          pl[n][w] = F16T::pack2(u0 - F16T::tof((uint16_t)pb[n][w]),
+                                 u1 - F16T::tof((uint16_t)(pb[n][w] >> 16)));
       }
-      po[n] = Bf16T::mfma16(onesv, pb[n], po[n]);
-      if constexpr (kSplitP) po[n] = Bf16T::mfma16(onesv, pl[n], po[n]);
+      po[n] = F16T::mfma16(onesv, pb[n], po[n]);
+      if constexpr (kSplitP) po[n] = F16T::mfma16(onesv, pl[n], po[n]);
     }
     // values: word w of the operand holds keys 2 w, 2 w + 1 of the lane's 8
     uint32_t vw[2][4][VW];
@@ -403,12 +436,12 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const u32x4_t vv = {U4Mfma<Bf16T>::pair(x[0], j), U4Mfma<Bf16T>::pair(x[1], j),
-                            U4Mfma<Bf16T>::pair(x[2], j), U4Mfma<Bf16T>::pair(x[3], j)};
+        const u32x4_t vv = {U4Value::pair(x[0], j), U4Value::pair(x[1], j),
+                            U4Value::pair(x[2], j), U4Value::pair(x[3], j)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          o[n][4 * half + j] = Bf16T::mfma16(vv, pb[n], o[n][4 * half + j]);
-          if constexpr (kSplitP) o[n][4 * half + j] = Bf16T::mfma16(vv, pl[n], o[n][4 * half + j]);
+          o[n][4 * half + j] = F16T::mfma16(vv, pb[n], o[n][4 * half + j]);
+          if constexpr (kSplitP) o[n][4 * half + j] = F16T::mfma16(vv, pl[n], o[n][4 * half + j]);
         }
       }
     }
@@ -521,7 +554,7 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
         v = none ? f32x4_t{0, 0, 0, 0} : v * (1.0f / sum);
         *reinterpret_cast<u32x2_t*>(a.out + at * D + d) =
             u32x2_t{DT::pack2(v[0], v[1]), DT::pack2(v[2], v[3])};
-        if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (mm + log2f(sum)) * kLn2;
+        if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : log_sum(mm, sum);
       } else {
         const int64_t at =
             ((((int64_t)b * c.kv_heads + head) * tiles + tile) * splits + split) * (16 * NT) +
@@ -599,7 +632,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(
   v = none ? f32x4_t{0, 0, 0, 0} : v * (1.0f / sum);
   *reinterpret_cast<u32x2_t*>(a.out + at * D + 4 * d) =
       u32x2_t{DT::pack2(v[0], v[1]), DT::pack2(v[2], v[3])};
-  if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
+  if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : log_sum(top, sum);
 }
 
 template <class DT, int D>

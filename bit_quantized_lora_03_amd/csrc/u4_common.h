@@ -77,7 +77,9 @@ __device__ __forceinline__ uint32_t u4_code(const U4Coder& u, double v, float t)
 // which costs bits of the fp32 sum: 7 at OFF = 128, where bf16's mantissa
 // ends at the code's last bit, 4 at OFF = 16, with the code at the
 // mantissa's top and one more shift for 8 codes.  Results that are rounded
-// to bf16 take 128; fp16 ones, and scores, which become exponents, 16.
+// to bf16 take 128; fp16 ones, and scores, which become exponents, 16.  The
+// attention's values, fp16 operands for both types of results, take 64, the
+// smallest without the additional shift.
 // The pairs of a word are (element j, element j + 4), j = 0..3.
 // (x & mask) | bits.  With both constant the compiler takes two instructions;
 // a constant whose origin it does not see sits in a register and takes one
@@ -115,6 +117,10 @@ struct U4Score<Bf16T> : U4Bits<0x4180, 3> {
 };
 template <>
 struct U4Score<F16T> : U4Mfma<F16T> {};
+struct U4Value : U4Bits<0x5400, 4> {  // with fp16 weights of the attention's values
+  static constexpr float kOff = 64.0f;
+  static constexpr uint32_t kOne = 0x3C003C00u;
+};
 // The 8 codes of a word as MFMA operand, in the order 0 4 1 5 2 6 3 7.
 template <class OP>
 __device__ __forceinline__ u32x4_t u4_expand8(uint32_t w) {
