@@ -54,12 +54,16 @@ def score_error(t, qv, scale):
     """How far the kernel's scores of a tile's rows can be off [R]: fp32 sums
     of D products with codes as 16 + c, scaled, with a few roundings of their
     own (the largest over the keys that a row sees)."""
-    D = qv.shape[-1]
-    aq = np.abs(qv[t["at"]]).sum(1)[:, None]
-    z = np.abs(scale * (qv[t["at"]] @ t["kv"].T))
-    mag = t["ks"] * (2 * 16 + 15) + np.abs(t["km"] - 16 * t["ks"])
-    dz = 2.0 ** -24 * ((D + 8) * abs(scale) * aq * mag[None] + 8 * z)
+    mag, z = score_sums(t, qv, scale)
+    dz = 2.0 ** -24 * ((qv.shape[-1] + 8) * mag + 8 * z)
     return np.max(np.where(t["see"], dz, 0.0), 1, initial=0.0)
+
+
+def score_sums(t, qv, scale):
+    """What a score's partial sums stay below, and the score's magnitude [R, L]."""
+    aq = np.abs(qv[t["at"]]).sum(1)[:, None]
+    mag = t["ks"] * (2 * 16 + 15) + np.abs(t["km"] - 16 * t["ks"])
+    return abs(scale) * aq * mag, np.abs(scale * (qv[t["at"]] @ t["kv"].T))
 
 
 def check_lse(pool, qv, lse, new, scale, causal=True, window=0):
@@ -98,3 +102,53 @@ class HostPool:
         c, p = c[:n, h].astype(np.float64), p[:n, h]
         s, m = u4.bits_value(p[:, 0]), u4.bits_value(p[:, 1])
         return m[:, None] + s[:, None] * c, s, m, c, np.ones(n, bool)
+
+
+def by_position(x, t):
+    """Values whose mean moves with their position, so that a share of the
+    keys that is lost or weighted wrongly moves the result by about one."""
+    return x + 2.0 * np.sin(t / 60.0)
+
+
+def check_rows(pool, qv, out, lse, new, dtype, scale, causal=True, window=0, name=""):
+    """Outputs and log sums of a call against fp64, with bars that an output of
+    zeros or one without some of the keys cannot pass.
+
+    What the roundings of single keys do to a result is a sum of independent
+    terms of either sign, a_t at most each; it passes 7 sqrt(sum a_t^2) once in
+    10^10 elements (Hoeffding).  The terms are
+      the weight p s as an operand: w e_p s |c - 8|, e_p 2^-11 (bf16), 2^-20 (fp16)
+      the score: 2 w |v - o| (exp, and the sum that it is divided by) times each of
+        its roundings, which are fewer than D / 4 + 8 (eight for each product of 32),
+        of 2^-23 of the largest partial sum at most; 2^-21 of the score's own size
+    fp32 sums are charged in full: a step adds 32 keys in one product, and a wave
+    walks every fourth one, so an accumulator is rounded fewer than n / 128 + 16
+    times (16: the product's own sum, the waves and the chunks), each time by
+    2^-23 of at most (2 72 + 15) sum(w s) (72: the codes' offset and the 8 taken
+    off); the eight keys' shares of 8 s + m are added one by one.  Last, half a
+    step of the output's type."""
+    u = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
+    ep = {"bf16": 2.0 ** -11, "f16": 2.0 ** -20}[dtype]
+    worst = 0.0
+    for t in tiles(pool, qv, new, scale, causal, window):
+        o, l = out[t["at"]], lse[t["at"]]
+        none = ~t["see"].any(1)
+        assert np.all(o[none] == 0) and np.all(l[none] == -np.inf), name
+        nan, dz = np.isnan(t["lse"]), score_error(t, qv, scale)
+        mag, z = score_sums(t, qv, scale)
+        dz2 = (qv.shape[-1] / 4 + 8) * (2.0 ** -23 * mag) ** 2 + (2.0 ** -21 * z) ** 2
+        assert np.isnan(o[nan]).all() and np.isnan(l[nan]).all(), name
+        for r in np.flatnonzero(~none & ~nan):
+            w, ro = t["w"][r][:, None], t["o"][r]
+            vs, vm = t["vs"][:, None], t["vm"][:, None]
+            single = w * w * ((ep * vs * (t["vc"] - 8)) ** 2 + 4 * dz2[r][:, None] * (t["vv"] - ro) ** 2)
+            n = int(t["see"][r].sum())
+            sums = ((n / 128 + 16) * 2.0 ** -23 * 159 * (w * vs).sum()
+                    + (n / 16 + 32) * 2.0 ** -24 * (w * np.abs(8 * vs + vm)).sum())
+            bar = u * np.abs(ro) + 7 * np.sqrt(single.sum(0)) + sums
+            assert np.all(np.isfinite(o[r])), (name, r)
+            off = np.abs(o[r] - ro)
+            worst = max(worst, float((off / bar).max()))
+            assert np.all(off <= bar), (name, r, float((off / bar).max()))
+            assert abs(l[r] - t["lse"][r]) <= dz[r] + 2.0 ** -20 * (1 + abs(t["lse"][r])), (name, r)
+    print(f"  {name}: worst error / bar {worst:.3f}", flush=True)
