@@ -18,10 +18,13 @@ constexpr int64_t kMaxK = int64_t{1} << 23;
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
 // A launch holds below 2^32 threads along x.  Of a product they are at most
 // 512 for 3 tiles of 16 rows; of a head vector a lane for 8 values; of the
-// attention 256 for a tile of 16 query rows.
+// attention 256 for a tile of 16 query rows; of the quantiser 256 for 4096
+// values and of the dequantiser 256 for 8192.
 constexpr int64_t kMaxN = int64_t{1} << 28;
 constexpr int64_t kMaxVectorValues = int64_t{1} << 34;
 constexpr int64_t kMaxQueryRows = int64_t{1} << 27;
+constexpr int64_t kMaxBlocks = (int64_t{1} << 24) - 1;  // of 256 threads
+constexpr int64_t kMaxQuantized = kMaxBlocks * 4096, kMaxDequantized = kMaxBlocks * 8192;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -71,7 +74,7 @@ int dequantize(const qlora_u4_weight* w, uint16_t* out, void* stream, bool f16) 
     if (!out) return QLORA_EINVAL;
     if (!aligned(out, 16)) return QLORA_EALIGN;
     const size_t n = (size_t)w->N * w->K;
-    if (n / 8192 > (size_t)kMaxGrid) return QLORA_ESHAPE;
+    if (n > (size_t)kMaxDequantized) return QLORA_ESHAPE;
     if (clash<1, 2>({{out, n * 2}}, {{w->codes, n / 2}, {w->pairs, n / w->group * 4}}))
       return QLORA_EINVAL;
     return hip_status(qlora::launch_dequantize_u4(w->codes, words(w->pairs), (int64_t)n, w->group,
@@ -305,7 +308,7 @@ int qlora_quantize_u4(const float* w, int64_t n_elems, int32_t group, uint8_t* c
   try {
     if (n_elems < 0) return QLORA_EINVAL;
     if (!group_ok(group)) return QLORA_ENOTSUP;
-    if (n_elems % group || n_elems / 4096 >= kMaxGrid) return QLORA_ESHAPE;
+    if (n_elems % group || n_elems > kMaxQuantized) return QLORA_ESHAPE;
     if (n_elems == 0) return QLORA_OK;
     if (!w || !codes || !pairs) return QLORA_EINVAL;
     if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(pairs, 16)) return QLORA_EALIGN;

@@ -403,13 +403,13 @@ typedef struct qlora_u4_weight {
 } qlora_u4_weight;
 
 /* fp32 w [n_elems] (a flattened [N, K] weight) to codes [n_elems/2] and
- * pairs [n_elems/group, 2].  n_elems must be a multiple of group (ESHAPE)
- * and may be 0 (nothing is enqueued).                                       */
+ * pairs [n_elems/group, 2].  n_elems must be a multiple of group, up to
+ * 2^36 - 4096 (ESHAPE), and may be 0 (nothing is enqueued).                 */
 int qlora_quantize_u4(const float* w, int64_t n_elems, int32_t group, uint8_t* codes,
                       uint16_t* pairs, void* stream);
 
 /* out [N, K] = the weight's values, m + s * c rounded once to fp32 and then
- * to bf16 (_f16: fp16), nearest even.                                       */
+ * to bf16 (_f16: fp16), nearest even.  N * K up to 2^37 - 8192 (ESHAPE).     */
 int qlora_dequantize_u4(const qlora_u4_weight* w, uint16_t* out, void* stream);
 int qlora_dequantize_u4_f16(const qlora_u4_weight* w, uint16_t* out, void* stream);
 
