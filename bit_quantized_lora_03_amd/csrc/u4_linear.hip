@@ -114,6 +114,7 @@ __global__ __launch_bounds__(64 * W) void linear_u4_kernel(
     return LPR == 8 ? piece ^ (row >> 1) : piece ^ (row >> 2);
   };
   auto store_w = [&] {
+    wave_exchange();  // the place's last reads: of x, or of the tile before
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int row = (64 / LPR) * i + cr;
@@ -122,6 +123,7 @@ __global__ __launch_bounds__(64 * W) void linear_u4_kernel(
 #pragma unroll
     for (int i = 0; i < NP; ++i)
       if (4 * i + ps < S::kPairs) st.w.p[pr][4 * i + ps] = pv[i];
+    wave_exchange();
   };
 
   const u32x4_t ones = {U4Mfma<DT>::kOne, U4Mfma<DT>::kOne, U4Mfma<DT>::kOne, U4Mfma<DT>::kOne};
@@ -135,6 +137,7 @@ __global__ __launch_bounds__(64 * W) void linear_u4_kernel(
         xv[q][t] = buffer_load16(xbuf, xo0 + (4 * t * xrow + u * U * 2 + 256 * q));
   };
   auto order_x = [&] {
+    wave_exchange();  // the last tile's reads
 #pragma unroll
     for (int q = 0; q < XP; ++q) {
 #pragma unroll
@@ -142,12 +145,14 @@ __global__ __launch_bounds__(64 * W) void linear_u4_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (4 * t + i < XQ) st.x[4 * i + xr][xs ^ (4 * i + xr)] = xv[q][4 * t + i];
+        wave_exchange();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           // product 4 q + c: of group g of the piece the lane's quarter
           const int g = c / C, e = c % C;
           xo[4 * q + c][t] = u4_order8(st.x[lr][(g * (G / 8) + lg * C + e) ^ lr]);
         }
+        wave_exchange();
       }
     }
     // a group's sums: the product with ones, whose columns are all alike
@@ -226,7 +231,7 @@ __global__ __launch_bounds__(64 * W) void linear_u4_kernel(
     for (int t = 0; t < NT; ++t) acc[(r * NT + t) * 64] = a[t];
   };
 
-  // LDS operations of one wave are in order, so its stage needs no barrier.
+  // A wave's stage is its own, so it needs no barrier of the block.
   // The next tile's codes and the next unit's x are on their way during a
   // tile's work.
   if (u0 < u1) {
