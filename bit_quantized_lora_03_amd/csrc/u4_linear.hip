@@ -301,13 +301,16 @@ void pick(const uint8_t* codes, const uint32_t* pairs, const uint16_t* x, int64_
     // short K.  N 8192, K 8192, M 1: 10.5 us against 12.5 with 8 waves;
     // N 22016: 24.3 against 21.1; N 2048, K 1024: 4.1, 3.3 with 8, 2.8 with 4.
     // Groups of 32 need the registers of 8 waves (N 4096, M 2: 7.1 against 5.9).
-    const bool wide = G > 32 && units >= 16 && N <= 16 * 256 * 3;
+    if constexpr (G > 32) {
+      if (units >= 16 && N <= 16 * 256 * 3) {
+        if (M == 1) QLORA_U4_GO(1, 1, 1, 16, 3, 1);
+        QLORA_U4_GO(1, 1, 4, 16, 3, 1);
+      }
+    }
     if (M == 1) {
-      if (wide) QLORA_U4_GO(1, 1, 1, 16, 3, 1);
       if (units >= 8) QLORA_U4_GO(1, 1, 1, 8, 4, 2);
       QLORA_U4_GO(1, 1, 1, 4, 4, 4);
     }
-    if (wide) QLORA_U4_GO(1, 1, 4, 16, 3, 1);
     if (units >= 8) QLORA_U4_GO(1, 1, 4, 8, 4, 2);
     QLORA_U4_GO(1, 1, 4, 4, 4, 4);
   }

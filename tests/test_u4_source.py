@@ -47,3 +47,12 @@ def test_lanes_of_a_wave_exchange_values_in_order():
     walk = text[text.index("if (u0 < u1) {"):]
     calls = re.findall(r"\b(order_x|store_w|work)\(", walk)
     assert calls[:2] == ["order_x", "store_w"] and set(calls[2:]) == {"work"}
+
+
+def test_no_variant_is_compiled_that_no_call_reaches():
+    """Groups of 32 take 8 waves or fewer, so the product's 16-wave variants
+    are instantiated for larger groups only."""
+    pick = body(source("u4_linear.hip"), "void pick(const uint8_t* codes")
+    wide = body(pick, "if constexpr (G > 32) ")
+    uses = re.findall(r"QLORA_U4_GO\(1, 1, \d, 16,", pick)
+    assert uses and uses == re.findall(r"QLORA_U4_GO\(1, 1, \d, 16,", wide)
