@@ -68,21 +68,33 @@ class U4Weight:
     (even element in the low nibble) and ``pairs`` bf16 [N, K/group, 2] (s
     and m; a value is m + s * code)."""
 
-    __slots__ = ("codes", "pairs", "N", "K", "group", "index", "struct")
+    __slots__ = ("codes", "pairs", "N", "K", "group", "index", "struct", "at")
 
     def __init__(self, codes, pairs):
         _dense(codes, "codes", _u8)
-        self.index = codes.get_device()
-        _dense(pairs, "pairs", _bf16, self.index)
+        index = codes.get_device()
+        _dense(pairs, "pairs", _bf16, index)
         cs, ps = codes.shape, pairs.shape
         if len(cs) != 2 or len(ps) != 3 or ps[0] != cs[0] or ps[2] != 2 or ps[1] == 0:
             raise ValueError("codes [N, K/2] and pairs [N, K/group, 2] are needed")
-        self.N, self.K = N, K = cs[0], 2 * cs[1]
-        self.group = group = K // ps[1]
+        N, K = cs[0], 2 * cs[1]
+        group = K // ps[1]
         if group not in GROUPS or group * ps[1] != K:
             raise ValueError(f"groups of {GROUPS} values are supported")
-        self.codes, self.pairs = codes, pairs
-        self.struct = U4Struct(codes.data_ptr(), pairs.data_ptr(), N, K, group)
+        self.codes, self.pairs, self.index = codes, pairs, index
+        self.N, self.K, self.group = N, K, group
+        c, p = codes.data_ptr(), pairs.data_ptr()
+        self.at = codes, c, pairs, p
+        self.struct = U4Struct(c, p, N, K, group)
+
+    def now(self) -> U4Struct:
+        """The descriptor of the tensors as they are: checked and written anew
+        where one was exchanged or has other memory since."""
+        codes, c, pairs, p = self.at
+        if self.codes is not codes or self.pairs is not pairs or codes.data_ptr() != c or \
+                pairs.data_ptr() != p:
+            self.__init__(self.codes, self.pairs)
+        return self.struct
 
     @property
     def device(self):
@@ -108,14 +120,16 @@ def quantize_u4(w, group: int = 64) -> U4Weight:
 def dequantize_u4(uw: U4Weight, dtype=torch.bfloat16):
     """U4Weight -> its values [N, K] in bf16 or fp16."""
     _need(dtype in _16BIT, "bf16 or fp16 values")
+    w = uw.now()
     out = torch.empty((uw.N, uw.K), dtype=dtype, device=uw.device)
-    _call("qlora_dequantize_u4", dtype, uw.index, uw.struct, out.data_ptr())
+    _call("qlora_dequantize_u4", dtype, uw.index, w, out.data_ptr())
     return out
 
 
 def linear_u4_fwd(uw: U4Weight, x, y=None):
     """y = x . W^T for few tokens: x [M, K] bf16 or fp16 (rows may be
     strided), y [M, N] of the same type (rows may be strided)."""
+    w = uw.now()
     dt, shape, N, K, index = x.dtype, x.shape, uw.N, uw.K, uw.index
     if dt not in _16BIT:
         raise ValueError("x has to be bf16 or fp16")
@@ -130,7 +144,7 @@ def linear_u4_fwd(uw: U4Weight, x, y=None):
               and (y.stride(1) == 1 or N == 1),
               f"y: [{M}, {N}] like x, with unit stride along N, is needed")
         ldy = y.stride(0) if M > 1 else N
-    _call("qlora_linear_u4_fwd", dt, index, uw.struct, x.data_ptr(), x.stride(0) if M > 1 else K,
+    _call("qlora_linear_u4_fwd", dt, index, w, x.data_ptr(), x.stride(0) if M > 1 else K,
           M, y.data_ptr(), ldy)
     return y
 
@@ -145,19 +159,18 @@ class Kv4Cache:
     kv_heads, page_size, 2], one pair per token and head."""
 
     __slots__ = ("k_codes", "k_pairs", "v_codes", "v_pairs", "pages", "kv_heads", "page_size",
-                 "head_dim", "index", "struct")
+                 "head_dim", "index", "struct", "at")
 
     def __init__(self, k_codes, k_pairs, v_codes, v_pairs):
         _dense(k_codes, "k_codes", _u8)
-        self.index = index = k_codes.get_device()
+        index = k_codes.get_device()
         _dense(k_pairs, "k_pairs", _bf16, index)
         _dense(v_codes, "v_codes", _u8, index)
         _dense(v_pairs, "v_pairs", _bf16, index)
         shape = k_codes.shape
         if len(shape) != 4:
             raise ValueError("codes [pages, kv_heads, page_size, head_dim / 2] are needed")
-        self.pages, self.kv_heads, self.page_size, half = pages, heads, size, half = shape
-        self.head_dim = 2 * half
+        pages, heads, size, half = shape
         pair = (pages, heads, size, 2)
         if v_codes.shape != shape or k_pairs.shape != pair or v_pairs.shape != pair:
             raise ValueError("codes and pairs of one cache differ in shape")
@@ -166,8 +179,20 @@ class Kv4Cache:
         if not 16 <= size <= 1024 or size & (size - 1):
             raise ValueError(f"page_size {size}: a power of two from 16 to 1024 is needed")
         self.k_codes, self.k_pairs, self.v_codes, self.v_pairs = k_codes, k_pairs, v_codes, v_pairs
-        self.struct = Kv4CacheStruct(k_codes.data_ptr(), k_pairs.data_ptr(), v_codes.data_ptr(),
-                                     v_pairs.data_ptr(), pages, size, heads, 2 * half)
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, 2 * half
+        self.index = index
+        self.at = at = (k_codes, k_codes.data_ptr(), k_pairs, k_pairs.data_ptr(),
+                        v_codes, v_codes.data_ptr(), v_pairs, v_pairs.data_ptr())
+        self.struct = Kv4CacheStruct(*at[1::2], pages, size, heads, 2 * half)
+
+    def now(self) -> Kv4CacheStruct:
+        """The descriptor of the tensors as they are (as :meth:`U4Weight.now`)."""
+        kc, kca, kp, kpa, vc, vca, vp, vpa = self.at
+        if self.k_codes is not kc or self.k_pairs is not kp or self.v_codes is not vc or \
+                self.v_pairs is not vp or kc.data_ptr() != kca or kp.data_ptr() != kpa or \
+                vc.data_ptr() != vca or vp.data_ptr() != vpa:
+            self.__init__(self.k_codes, self.k_pairs, self.v_codes, self.v_pairs)
+        return self.struct
 
     @property
     def device(self):
@@ -226,6 +251,7 @@ def kv4_append(cache: Kv4Cache, k, v, cu_q, seq_lens, block_table, max_q: int, q
     dt = k.dtype
     if dt not in _16BIT:
         raise ValueError("k, v and q have to be bf16 or fp16")
+    pool = cache.now()
     T, _, kts, khs = _rows(cache, k, "k", dt, -1, cache.kv_heads)
     _, _, vts, vhs = _rows(cache, v, "v", dt, T, cache.kv_heads)
     qp = op = None
@@ -248,7 +274,7 @@ def kv4_append(cache: Kv4Cache, k, v, cu_q, seq_lens, block_table, max_q: int, q
         rows, rot = cos_sin.shape
         tp = cos_sin.data_ptr()
     bt = _batch(cache, cu_q, seq_lens, block_table, max_q, T)
-    _call("qlora_kv4_append", dt, cache.index, cache.struct, bt, k.data_ptr(), kts, khs,
+    _call("qlora_kv4_append", dt, cache.index, pool, bt, k.data_ptr(), kts, khs,
           v.data_ptr(), vts, vhs, qp, qts, qhs, heads, tp, rows, rot, 1 if interleaved else 0, op)
     return q_out
 
@@ -260,11 +286,12 @@ def kv4_read(cache: Kv4Cache, cu_q, seq_lens, block_table, max_q: int, rows: int
     cu_q[-1] are uninitialised."""
     _need(dtype in _16BIT, "bf16 or fp16 values")
     _need(rows >= 0, "rows is negative")
+    pool = cache.now()
     bt = _batch(cache, cu_q, seq_lens, block_table, max_q, rows)
     shape, device = (rows, cache.kv_heads, cache.head_dim), cu_q.device
     k = torch.empty(shape, dtype=dtype, device=device)
     v = torch.empty(shape, dtype=dtype, device=device)
-    _call("qlora_kv4_read", dtype, cache.index, cache.struct, bt, k.data_ptr(), v.data_ptr())
+    _call("qlora_kv4_read", dtype, cache.index, pool, bt, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -287,6 +314,7 @@ def kv4_attention(cache: Kv4Cache, q, cu_q, seq_lens, block_table, max_q: int, m
     dt = q.dtype
     if dt not in _16BIT:
         raise ValueError("q has to be bf16 or fp16")
+    pool = cache.now()
     T, heads, qts, qhs = _rows(cache, q, "q", dt, -1, -1)
     D, index, device = cache.head_dim, cache.index, q.device
     bt = _batch(cache, cu_q, seq_lens, block_table, max_q, T)
@@ -310,7 +338,7 @@ def kv4_attention(cache: Kv4Cache, q, cu_q, seq_lens, block_table, max_q: int, m
     else:
         _dense(workspace, "workspace", _u8, index)
         need = workspace.numel()
-    _call("qlora_kv4_attention", dt, index, cache.struct, bt, q.data_ptr(), qts, qhs, heads,
+    _call("qlora_kv4_attention", dt, index, pool, bt, q.data_ptr(), qts, qhs, heads,
           D ** -0.5 if scale is None else scale, 1 if causal else 0, window, max_len,
           out.data_ptr(), None if lse is None else lse.data_ptr(),
           None if workspace is None else workspace.data_ptr(), need)
