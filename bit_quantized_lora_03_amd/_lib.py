@@ -576,11 +576,11 @@ def merge_adapter(base, A, B, alpha: float, out_f32: bool = True, out_bf16: bool
     original weights).  Returns ``(fp32 [N, K] or None, bf16 bits [N, K]
     (int16) or None, PackedWeight, U4Weight or None)``; the last is the fp32
     merge quantised again (needs the fp32 output): to NF4 with
-    ``requantize=True``, to the 4-bit group format (groups of 64) with
-    ``requantize="u4"``."""
+    ``requantize=True`` or ``"nf4"``, to the 4-bit group format (groups of 64)
+    with ``requantize="u4"``; other texts are refused."""
     torch = _torch()
-    if isinstance(requantize, str) and requantize != "u4":
-        raise ValueError(f"requantize: True, False or 'u4', not {requantize!r}")
+    if isinstance(requantize, str) and requantize not in ("", "nf4", "u4"):
+        raise ValueError(f"requantize: True, False, 'nf4' or 'u4', not {requantize!r}")
     if requantize and not out_f32:
         raise ValueError("requantize needs the fp32 merge")
     packed = isinstance(base, PackedWeight)
