@@ -24,6 +24,7 @@ _u8, _i32, _f32, _bf16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 _current = torch._C._cuda_getDevice
 _stream = torch._C._cuda_getCurrentRawStream
 _entry = {}
+_I32 = 2 ** 31  # ctypes would cut larger ones to their low bits
 
 
 def _call(name: str, dtype, index: int, *args) -> None:
@@ -214,8 +215,10 @@ def _batch(cache: Kv4Cache, cu_q, seq_lens, block_table, max_q: int, rows: int) 
     cs, ls, bs = cu_q.shape, seq_lens.shape, block_table.shape
     if len(ls) != 1 or len(cs) != 1 or len(bs) != 2 or cs[0] != ls[0] + 1 or bs[0] != ls[0]:
         raise ValueError("cu_q [B + 1], seq_lens [B] and block_table [B, width] are needed")
-    if not 0 <= max_q < 2 ** 31:
+    if not 0 <= max_q < _I32:
         raise ValueError(f"max_q {max_q} is out of range")
+    if ls[0] >= _I32 or bs[1] >= _I32:
+        raise ValueError(f"block_table {tuple(bs)} is out of range")
     return Kv4BatchStruct(cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), rows,
                           ls[0], bs[1], max_q)
 
@@ -231,6 +234,8 @@ def _rows(cache: Kv4Cache, t, name: str, dtype, rows: int, heads: int):
                          f"{'heads' if heads < 0 else heads}, {cache.head_dim}] of {dtype} on "
                          f"{cache.device} is needed, got {tuple(shape)} of {t.dtype} on {t.device}")
     ts, hs, ds = t.stride()
+    if shape[1] >= _I32:
+        raise ValueError(f"{name}: {shape[1]} heads are out of range")
     if ds != 1:
         raise ValueError(f"{name}: unit stride along head_dim is needed")
     # the stride of an axis of length one says nothing
@@ -272,6 +277,7 @@ def kv4_append(cache: Kv4Cache, k, v, cu_q, seq_lens, block_table, max_q: int, q
         _need(cos_sin.dim() == 2, "cos_sin: [positions, rot] is needed")
         _dense(cos_sin, "cos_sin", _f32, cache.index)
         rows, rot = cos_sin.shape
+        _need(rot < _I32, f"cos_sin: {rot} columns are out of range")
         tp = cos_sin.data_ptr()
     bt = _batch(cache, cu_q, seq_lens, block_table, max_q, T)
     _call("qlora_kv4_append", dt, cache.index, pool, bt, k.data_ptr(), kts, khs,
@@ -297,8 +303,12 @@ def kv4_read(cache: Kv4Cache, cu_q, seq_lens, block_table, max_q: int, rows: int
 
 def kv4_attention_workspace_bytes(seqs: int, max_q: int, max_len: int, q_heads: int,
                                   kv_heads: int, head_dim: int, window: int = 0) -> int:
-    if not -2 ** 31 <= window < 2 ** 31:  # a negative one is the library's to refuse
-        raise ValueError(f"window {window} is out of range")
+    # what is negative is the library's to refuse
+    for n, v in (("q_heads", q_heads), ("kv_heads", kv_heads), ("head_dim", head_dim),
+                 ("window", window)):
+        _need(-_I32 <= v < _I32, f"{n} {v} is out of range")
+    for n, v in (("seqs", seqs), ("max_q", max_q), ("max_len", max_len)):
+        _need(-2 ** 63 <= v < 2 ** 63, f"{n} {v} is out of range")
     return int(_lib.lib().qlora_kv4_attention_workspace_bytes(seqs, max_q, max_len, q_heads,
                                                               kv_heads, head_dim, window))
 
@@ -328,8 +338,9 @@ def kv4_attention(cache: Kv4Cache, q, cu_q, seq_lens, block_table, max_q: int, m
               and lse.get_device() == index, f"lse: fp32 [{T}, {heads}] is needed")
     elif return_lse:
         lse = torch.empty((T, heads), dtype=_f32, device=device)
-    if not -2 ** 31 <= window < 2 ** 31:  # a negative one is the library's to refuse
-        raise ValueError(f"window {window} is out of range")
+    # what is negative is the library's to refuse
+    if not -_I32 <= window < _I32 or not -2 ** 63 <= max_len < 2 ** 63:
+        raise ValueError(f"window {window} or max_len {max_len} is out of range")
     need = _lib.lib().qlora_kv4_attention_workspace_bytes(bt.seqs, max_q, max_len, heads,
                                                           cache.kv_heads, D, window)
     if workspace is None:
