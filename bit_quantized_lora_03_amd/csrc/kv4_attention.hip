@@ -58,7 +58,7 @@ namespace qlora {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kStep = 32;
+constexpr int kStep = kKv4Step;
 constexpr float kSlack = 8.0f;
 constexpr float kMid = 8.0f;
 // With E the power of two at or above the row's largest s' (at least
@@ -70,32 +70,6 @@ constexpr float kUp = 6.0f;
 constexpr float kLeastStep = 0x1p-60f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-
-// The keys of a tile of query rows: [lo, hi), lo a multiple of 32, cut into
-// n chunks of `chunk` keys.
-struct Span {
-  int lo, hi, chunk, n;
-  int i0, i1;  // first and last query token of the tile
-};
-__device__ __forceinline__ Span kv4_span(const Kv4Seq& sq, const Kv4AttnArg& a, int group,
-                                         int r0, int tile, int chunk, int splits) {
-  Span s;
-  const int last = (int)sq.n * group - 1;
-  s.i0 = r0 / group;
-  s.i1 = min(r0 + tile - 1, last) / group;
-  // the table's last key bounds what can be read
-  int64_t hi = min(sq.len, a.table_keys), lo = 0;
-  if (a.causal) hi = min(hi, sq.pos0 + s.i1 + 1);
-  if (a.window > 0) lo = max(lo, sq.pos0 + s.i0 - a.window + 1);
-  s.hi = (int)max(hi, (int64_t)0);
-  s.lo = (int)(lo & ~(int64_t)(kStep - 1));
-  const int keys = max(s.hi - s.lo, 0);
-  // a sequence longer than the call was planned for takes larger chunks
-  const int need = (keys + splits - 1) / splits;
-  s.chunk = max(chunk, (need + kStep - 1) / kStep * kStep);
-  s.n = (keys + s.chunk - 1) / s.chunk;
-  return s;
-}
 
 // A wave's LDS: a ring of stages, each with one step's keys, values (32 rows
 // of D / 2 bytes) and their pairs (16 words each: keys of both halves, values
@@ -242,7 +216,7 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
   if (r0 >= rows) return;
   const Span sp = kv4_span(sq, a, group, r0, 16 * NT, chunk, splits);
   if (split > 0 && split >= sp.n) return;
-  const int t0 = sp.lo + split * sp.chunk, t1 = min(t0 + sp.chunk, sp.hi);
+  const int t0 = sp.begin(split), t1 = sp.end(split);
 
   // this lane's query rows (past the last: the last again, not stored)
   u32x4_t q[NT][KC];

@@ -1,0 +1,54 @@
+"""Lengths far past the block table: the tokens that are not there are not
+attended to, whatever the window leaves."""
+
+import numpy as np
+import pytest
+
+import bit_quantized_lora_03_amd as q
+from tests.gpu_util import Guarded
+from tests.test_gpu_kv4 import Pool
+from tests.test_gpu_u4 import to_dev
+
+pytestmark = pytest.mark.gpu
+
+TOP = 2 ** 31 - 1
+
+
+def run(cache, qq, lens, table, new, window, max_len, causal=True):
+    import torch
+    cu = to_dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32))
+    out, lse = Guarded(qq.shape, qq.dtype), Guarded(qq.shape[:2], torch.float32)
+    q.kv4_attention(cache, qq, cu, to_dev(np.array(lens, np.int32)), table, max(new), max_len,
+                    window=window, causal=causal, out=out.t, lse=lse.t)
+    out.check("out")
+    lse.check("lse")
+    return out.t, lse.t
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("length", [TOP, TOP - 31, TOP - 300, 2 ** 30 + 17, 2 ** 30])
+@pytest.mark.parametrize("max_len", [48, 2 ** 20, 2 ** 30])
+def test_window_behind_the_table(cuda, D, length, max_len):
+    import torch
+    pool = Pool([48, 33, 48], 16, 2, D, seed=D).fill()
+    cache, table, new = pool.cache(), to_dev(pool.table), [1, 1, 3]
+    qq = torch.randn(5, 4, D, device="cuda").to(torch.bfloat16)
+    for window in (1, 40, 4096):
+        out, lse = run(cache, qq, [length, 33, length], table, new, window, max_len)
+        for rows in (slice(0, 1), slice(2, 5)):
+            assert (out[rows] == 0).all() and (lse[rows] == -float("inf")).all()
+        want, wl = run(cache, qq, [0, 33, 0], table, new, window, max_len)
+        assert torch.equal(out[1], want[1]) and torch.equal(lse[1], wl[1])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_all_of_the_table_of_a_longer_sequence(cuda, causal):
+    """Without a window, or with one that reaches back to token 1."""
+    import torch
+    pool = Pool([48, 33], 16, 2, 128, seed=3).fill()
+    cache, table = pool.cache(), to_dev(pool.table)
+    qq = torch.randn(2, 4, 128, device="cuda").to(torch.bfloat16)
+    for length, window, same in ((TOP, 0, 0), (2 ** 30 + 5, 0, 0), (TOP, TOP - 1, 47)):
+        out, lse = run(cache, qq, [length, 33], table, [1, 1], window, 100, causal)
+        want, wl = run(cache, qq, [48, 33], table, [1, 1], same, 100, causal)
+        assert torch.equal(out[0], want[0]) and torch.equal(lse[0], wl[0]), (length, window)
