@@ -23,8 +23,10 @@ __host__ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4BatchArg& bt, int b)
   q.row0 = first;
   q.len = bt.seq_lens[b];
   q.pos0 = q.len - (last - first);
-  // a start before row 0 leaves nothing; rows past T are left out
-  q.n = first < 0 ? 0 : (last < bt.rows ? last : bt.rows) - first;
+  // a start before row 0 or behind the end leaves nothing; rows past T are
+  // left out
+  q.n = (last < bt.rows ? last : bt.rows) - first;
+  if (first < 0 || q.n < 0) q.n = 0;
   if (q.n > bt.max_q) q.n = bt.max_q;
   return q;
 }

@@ -52,3 +52,32 @@ def test_all_of_the_table_of_a_longer_sequence(cuda, causal):
         out, lse = run(cache, qq, [length, 33], table, [1, 1], window, 100, causal)
         want, wl = run(cache, qq, [48, 33], table, [1, 1], same, 100, causal)
         assert torch.equal(out[0], want[0]) and torch.equal(lse[0], wl[0]), (length, window)
+
+
+@pytest.mark.parametrize("cu", [[TOP, 0, 0], [0, TOP, -TOP - 1], [-TOP - 1, TOP, 3], [5, 2, 0],
+                                [TOP - 8, -TOP - 1, TOP], [5, 9, 5]])
+@pytest.mark.parametrize("Hq,Hkv", [(16, 2), (8, 1), (3, 1)])
+def test_rows_that_do_not_ascend(cuda, cu, Hq, Hkv):
+    """Nothing outside the call's rows is read or written, and rows that no
+    sequence has stay as they were."""
+    import torch
+    D, T = 64, 5
+    pool = Pool([48, 48], 16, Hkv, D, seed=7).fill()
+    cache, table = pool.cache(), to_dev(pool.table)
+    qq, k = (torch.randn(T, h, D, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv))
+    out, lse = Guarded(qq.shape, qq.dtype), Guarded(qq.shape[:2], torch.float32)
+    before = out.t.clone().view(torch.int16)
+    batch = to_dev(np.array(cu, np.int32)), to_dev(np.array([48, 48], np.int32)), table
+    for max_len in (48, 1 << 16):
+        q.kv4_attention(cache, qq, *batch, 4, max_len, out=out.t, lse=lse.t)
+    out.check("out")
+    lse.check("lse")
+    mine = np.zeros(T, bool)
+    for a, b in zip(cu, cu[1:]):
+        if a >= 0:
+            mine[a:min(max(b, a), T, a + 4)] = True
+    same = (out.t.view(torch.int16) == before).all(-1).all(-1).cpu().numpy()
+    assert np.array_equal(same, ~mine)
+    q.kv4_append(cache, k, k, *batch, 4, q=qq, q_out=out.t)
+    q.kv4_read(cache, *batch, 4, T)
+    out.check("q_out")

@@ -84,3 +84,15 @@ def test_keys_stay_inside_the_table(look, causal, window):
                         assert s["t0"] == at and at % 32 == 0 and at < s["t1"] <= hi, (case, s)
                         at = s["t1"]
                     assert at == hi, case
+
+
+def test_rows_stay_inside_the_tensors(look):
+    edge = [-TOP - 1, -1, 0, 1, 5, 99, 100, 101, TOP - 1, TOP]
+    for first in edge:
+        for last in edge:
+            for length in LENS:
+                # a negative number times the query heads of a KV head can be
+                # anything in 32 bits: -(2^31 - 1) rows of 8 heads were 8
+                s = look([first, last], [length], 100, 9, 4096, 1, 0, 8, 0, 16, 256, 4, 0)
+                assert 0 <= s["n"] <= 9, (first, last, s)
+                assert s["n"] == 0 or 0 <= s["row0"] <= 100 - s["n"], (first, last, s)
