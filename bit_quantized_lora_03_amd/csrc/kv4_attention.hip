@@ -24,17 +24,17 @@
 // by c' - 8 and not by c'.
 // p s' is an fp16 operand (half a step is 2^-11): as a bf16 one (2^-8) it took
 // bf16 outputs 2.4e-3 from the 64-bit result; now they are 1.7e-3 off, as the
-// exact result rounded is (64 ragged sequences 101 us with either, many rows 3
-// to 4 % slower).  fp16 outputs take a second operand for what the first loses
-// (2^-22).  fp16's range is narrow, so the exponent that p is counted from
-// holds the largest s' of the row so far beside the largest score (kUp,
-// kLeastStep below).
+// exact result rounded is (64 ragged sequences 103 us with either, many rows 3
+// to 6 % slower).  fp16 outputs take a second operand for what the first loses
+// (2^-22).  fp16's range is narrow, so M follows the row's largest p s' and
+// not its largest p (kUp below): what is small in fp16 is small beside the
+// largest share of the result, whatever the steps are.
 //
 // A wave walks 32 keys a step.  Keys, values and pairs come to its own LDS by
 // DMA two steps ahead (one at D = 256): a step's 4.3 KiB (D 128) in 8
-// instructions and no registers.  The running maximum is only moved when a
-// score passes it by 2^kSlack, and the largest s' goes up by powers of two, so
-// the accumulators are hardly ever rescaled.  Four waves of a block
+// instructions and no registers.  M is a whole number that is only moved when
+// some p s' passes 2^kMost, then far enough for it to grow 2^8 times, so the
+// accumulators are hardly ever rescaled, and exactly.  Four waves of a block
 // interleave their steps and join in LDS; long axes are cut into chunks whose
 // partial results a second kernel joins in chunk order (no atomics: every run
 // gives the same bits).
@@ -59,15 +59,12 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kStep = kKv4Step;
-constexpr float kSlack = 8.0f;
 constexpr float kMid = 8.0f;
-// With E the power of two at or above the row's largest s' (at least
-// kLeastStep), p is counted as 2^(z log2 e - M + kUp) / E: p s' then is at most
-// 2^(kSlack + kUp) = 2^14, inside fp16, and 2^kUp at the running maximum, 2^20
-// above the smallest normal fp16.  (p itself, and sums of p, pass fp32's range
-// only where steps pass 2^100, or where all are below 2^-60.)
-constexpr float kUp = 6.0f;
-constexpr float kLeastStep = 0x1p-60f;
+// M is the row's largest z log2 e + log2 s', rounded up, less kUp: its largest
+// p s' is 2^kUp, 2^20 times the smallest normal fp16 number, and moves M again
+// when it would pass 2^kMost, inside fp16.  With small steps M stays at the
+// largest z log2 e less kUnder, so that sums of p stay inside fp32.
+constexpr float kUp = 6.0f, kMost = 14.0f, kUnder = 60.0f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -249,20 +246,18 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
   const int all_hi = (int)max(a.causal ? min(sq.len, sq.pos0 + sp.i0 + 1) : sq.len, (int64_t)0);
 
   f32x4_t o[NT][VC], po[NT];
-  float m[NT], mu[NT], l[NT], cs[NT], big[NT];
+  float gate[NT], mu[NT], l[NT], cs[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int j = 0; j < VC; ++j) o[n][j] = f32x4_t{0, 0, 0, 0};
     po[n] = f32x4_t{0, 0, 0, 0};
-    m[n] = -INFINITY;  // running maximum of the products q.k
-    mu[n] = 0.0f;      // what p is counted from, in log2 units; 0 while m is -inf
-    big[n] = kLeastStep;  // the power of two at or above every s' so far
+    mu[n] = 0.0f;         // M, 0 while nothing has been seen
+    gate[n] = -INFINITY;  // M + kMost, -inf while nothing has been seen
     l[n] = cs[n] = 0.0f;
   }
   // never 0, which would make a hidden score, -inf, NaN; 2^-100 is as good
   const float c1 = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);
-  const float slack = kSlack / c1;
   // where the lane reads its part of a stage
   uint32_t koff[D == 256 ? 2 : 1], voff[4];
   if constexpr (D == 64) {
@@ -341,17 +336,25 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
           vs[h][i] = u4_s(vp[h][i]);
           most = fmaxf(most, fabsf(vs[h][i]));
         }
-      if (__any(top > m[n] + slack || most > big[n])) {
-        top = fmaxf(column_max(top), m[n]);
-        const float was = m[n] == -INFINITY ? -INFINITY : mu[n];
-        m[n] = top;
-        // the power of two above `most`; NaN and infinities leave it, whose sums
-        // are not finite anyway
-        const uint32_t e = __float_as_uint(column_max(most)) & 0x7F800000u;
-        big[n] = fmaxf(big[n], e < 0x7F000000u ? __uint_as_float(e + 0x00800000u) : 0x1p127f);
-        const int up = (int)(__float_as_uint(big[n]) >> 23) - 127;
-        mu[n] = top == -INFINITY ? 0.0f : fmaf(top, c1, (float)up - kUp);
-        const float f = __builtin_amdgcn_exp2f(was - mu[n]);
+      // the lane's largest p and s' bound its products
+      if (__any(fmaf(top, c1, fmaxf(__builtin_amdgcn_logf(most), kMost - kUnder)) > gate[n])) {
+        float r = -INFINITY;  // the largest z log2 e + log2 s'
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            r = fmaxf(r, fmaf(z[n][h][i], c1, __builtin_amdgcn_logf(fabsf(vs[h][i]))));
+        r = column_max(r);
+        top = column_max(top) * c1;
+        // a row that has seen nothing stays so, and one whose products do not
+        // pass has its M
+        const bool move = fmaxf(r, top + (kMost - kUnder)) > gate[n];
+        const float to = fmaxf(ceilf(r) - kUp, ceilf(top) - kUnder);
+        const float f = !move                  ? 1.0f
+                        : gate[n] == -INFINITY ? 0.0f
+                                               : __builtin_amdgcn_exp2f(mu[n] - to);
+        mu[n] = move ? to : mu[n];
+        gate[n] = move ? to + kMost : gate[n];
 #pragma unroll
         for (int j = 0; j < VC; ++j)
 #pragma unroll
@@ -472,9 +475,10 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
     }
   }
 
-  // join the four waves, their maxima in log2 units
+  // join the four waves
+  float m[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) m[n] = m[n] == -INFINITY ? m[n] : mu[n];
+  for (int n = 0; n < NT; ++n) m[n] = gate[n] == -INFINITY ? -INFINITY : mu[n];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     l[n] = column_sum(l[n]);

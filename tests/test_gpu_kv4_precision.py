@@ -119,3 +119,53 @@ def test_steps_behind_the_length_have_no_effect(cuda):
     again = attend(pool, [3], 4, "bf16")[1:]
     for a, b in zip(first, again):
         assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("at,score,size", [
+    (0, -70.0, 40), (300, -70.0, 40), (517, -30.0, 30), (3, 0.0, 0), (1000, -120.0, 90)])
+def test_large_values_without_weight(cuda, D, dtype, at, score, size):
+    """One visible token whose values are 2^size larger but whose score leaves
+    it next to no weight: the others' values lose nothing.  Before the first
+    token with weight, among them and last."""
+    import torch
+    n, L = 1, 1100
+    pool = steps_pool(lambda t: np.where(t == at, 2.0 ** size, 1.0), [L], D)
+    qq = strided(n, 1, D, tdtype(dtype), np.random.default_rng(9), 8)
+    x = f64(qq)[0, 0]
+    if score:
+        k = x * (score * D ** 0.5 / (x @ x))
+        c, p = u4.encode(k[None])
+        where = pool.table[0, at // 16], 0, at % 16
+        pool.codes["k"][where], pool.pairs["k"][where] = u4.pack(c[0]), p[0]
+    for max_len in (L, 100000):
+        out, lse = Guarded(qq.shape, tdtype(dtype)), Guarded(qq.shape[:2], torch.float32)
+        q.kv4_attention(pool.cache(), qq, *pool.ints([n]), 1, max_len, out=out.t, lse=lse.t)
+        ro, _ = ref.outputs(pool, f64(qq), [n], SCALE[D])
+        assert np.abs(ro).max() < 4                  # the token is not in the result
+        check_norm(f"{dtype} D{D} {at} {score} 2^{size}", f64(out.t), ro, dtype)
+        ref.check_lse(pool, f64(qq), f64(lse.t), [n], SCALE[D])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_and_steps_against_each_other(cuda, D):
+    """Scores that rise by 2^200 along the axis while the steps fall by 2^100,
+    and the other way round."""
+    import torch
+    L = 900
+    for sign in (1.0, -1.0):
+        pool = steps_pool(lambda t: 2.0 ** (-sign * (t - 450) / 9.0), [L], D)
+        qq = strided(1, 1, D, torch.bfloat16, np.random.default_rng(9), 8)
+        x = f64(qq)[0, 0]
+        scores = sign * np.linspace(-70, 70, L)
+        c, p = u4.encode(x[None] * (scores[:, None] * D ** 0.5 / (x @ x)))
+        for t in range(L):
+            where = pool.table[0, t // 16], 0, t % 16
+            pool.codes["k"][where], pool.pairs["k"][where] = u4.pack(c[t]), p[t]
+        for max_len in (L, 100000):
+            out, lse = Guarded(qq.shape, torch.bfloat16), Guarded(qq.shape[:2], torch.float32)
+            q.kv4_attention(pool.cache(), qq, *pool.ints([1]), 1, max_len, out=out.t, lse=lse.t)
+            ro, _ = ref.outputs(pool, f64(qq), [1], SCALE[D])
+            check_norm(f"D{D} {sign}", f64(out.t), ro, "bf16")
+            ref.check_lse(pool, f64(qq), f64(lse.t), [1], SCALE[D])
