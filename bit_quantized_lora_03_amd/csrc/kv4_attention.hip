@@ -39,15 +39,17 @@
 // partial results a second kernel joins in chunk order (no atomics: every run
 // gives the same bits).
 //
-// Measured (graph replays; in brackets a copy of the same bytes): 64 ragged
-// sequences up to 8192 keys, 32 heads on 8, D 128, bf16: 101 us (80), the
-// join 7 of it; 2 x 131071 keys, 64 heads on 8, fp16: 66 (48), the join 9;
-// one sequence of 777, 16 heads, D 64: 9.4, two launches and their first
-// loads.  A step's 320 vector instructions (130 for expanding the codes, 150
-// for scores and weights) and 17 MFMAs take about two thirds of the time that
-// its bytes do; what is left is the start of a block, four dependent loads
-// long.  Many rows are bound by the vector instructions: 3 x 251 rows of 16
-// heads on 4, D 256, window 4096: 106 us, 0.36 PFLOP/s.
+// Measured (calls from Python that follow each other; in brackets a copy of
+// the same bytes): 64 ragged sequences up to 8192 keys, 32 heads on 8, D 128,
+// bf16: 98 us (80), the join 5 of it; 2 x 131071 keys, 64 heads on 8, fp16: 65
+// (48), the join 7; one sequence of 777, 16 heads, D 64: 9.6 in a replayed
+// graph, two launches and their first loads.  A step's 290 vector instructions
+// (130 for expanding the codes) keep the vector units busy for half of the
+// time at 64 sequences; what is left is the start of a block, four dependent
+// loads long, and the ragged ends.  Many rows: 3 x 251 rows of 16 heads on 4, D
+// 256, window 4096: 101 us, 0.38 PFLOP/s; 440 vector instructions for 33 MFMAs
+// a step, which take 83 % of the time while a SIMD has its two waves and 53 %
+// of all of it, for 756 blocks are one and a half rounds.
 
 #include <algorithm>
 
@@ -656,15 +658,18 @@ Kv4AttnPlan kv4_attn_plan(int64_t seqs, int64_t max_q, int64_t max_len, int q_he
   int64_t keys = max_len;
   // a tile's window starts up to 31 keys early
   if (window > 0 && window + max_q + kStep < keys) keys = window + max_q + kStep;
-  // Chunks for two rounds of the chip's blocks (three blocks a CU), so that
-  // the short sequences of a ragged batch do not leave it idle, of at least
-  // two steps for each wave: 64 ragged sequences up to 8192, 8 heads: 101 us,
-  // with one round 109, with five 117.  Full tiles of rows, whose partial
-  // results are more of the work, for one round: 3 x 251 rows, window 4096, D
-  // 256: 106 us with one chunk, 126 with two; 700 rows on 8000 keys, D 128:
-  // 200 and 207.  Their number is rounded to the nearest: a last chunk of few
-  // keys costs all the partial results (3 x 500 rows, 1512 blocks: 205 us with
-  // a second chunk, 126 without).
+  // As many chunks as make 1536 blocks, so that the short sequences of a
+  // ragged batch do not leave the chip idle, of at least two steps for each
+  // wave: 64 ragged sequences up to 8192, 8 heads: 101 us, with 768 blocks
+  // wanted 109, with 3840 117.  Full tiles of rows, whose partial results are
+  // more of the work, as make 768: 3 x 251 rows, window 4096, D 256: 106 us
+  // with one chunk, 126 with two; 700 rows on 8000 keys, D 128: 200 and 207.
+  // Both are what measured best and not whole rounds: a CU has room for five
+  // blocks at D 64, three at D 128 and two at D 256 and with two column tiles.
+  // The number of chunks is rounded to the nearest: a last chunk of few keys
+  // costs all the partial results (3 x 500 rows, 1512 blocks: 205 us with a
+  // second chunk, 126 without).  Every sequence is taken to have max_q rows:
+  // beside one long prompt the others' keys are not cut.
   const int64_t want = rows >= 64 ? 768 : 1536;
   constexpr int64_t kPer = kStep * kWaves;
   const int64_t base = std::max<int64_t>(seqs * kv_heads * p.tiles, 1);

@@ -28,10 +28,13 @@
 //
 // Measured (graph replays, weights from HBM; in brackets a copy of the same
 // bytes): M 1, 4096 x 4096, groups of 64: 4.8 us (2.0); M 1, 8192 x 8192:
-// 10.5 (7.9); M 4, 22016 x 8192: 25 (21.3); M 16, 8192 x 8192: 14.4 (7.6),
-// where x, 256 KiB for each block, is twice the codes' traffic into the CUs;
-// M 61, 11008 x 4096, groups of 32: 25 (6.3), bound by the vector
-// instructions that decode the codes and scale the sums.
+// 10.5 (7.9); M 4, 22016 x 8192: 25 (21.3); M 16, 8192 x 8192: 14.4 (7.6);
+// M 61, 11008 x 4096, groups of 32: 25 (6.3).  Neither of the last two is
+// bound by one unit.  While its two waves are there, a SIMD's vector
+// instructions take 40 % of the time (M 16) and 39 % (M 61), its matrix core 13
+// and 21 %, the LDS that the block's eight waves share 34 and 40 %, and a wave
+// waits for 45 and 33 % of it: two waves a SIMD are too few to hide one behind
+// the others, and every block reads all of x, at M 16 twice the codes' bytes.
 
 #include "launch.h"
 #include "u4_common.h"
@@ -316,7 +319,9 @@ void pick(const uint8_t* codes, const uint32_t* pairs, const uint16_t* x, int64_
   }
   // more tokens: x is most of what a block reads, so a block keeps as many
   // rows as it can (M 16, N 22016, K 8192: 27.6 us with six tiles, 32.1 with
-  // three)
+  // three).  With groups of 32 the variant for 17 to 32 tokens has all 256
+  // registers and 28 more in scratch memory, some of them in the loop over K
+  // (N 11008, K 4096, M 32: 20.0 us).
   if (M <= 16) QLORA_U4_GO(1, 4, 4, 8, 8, 1);
   if (M <= 32) QLORA_U4_GO(2, 8, 4, 8, 6, 1);
   QLORA_U4_GO(4, 16, 4, 8, 3, 1);

@@ -418,9 +418,12 @@ int qlora_dequantize_u4_f16(const qlora_u4_weight* w, uint16_t* out, void* strea
  * multiple of 8, EALIGN, up to 2^23, ESHAPE; y needs the alignment of its
  * type only).  The
  * weight's values enter exactly (never rounded to 16 bits), sums are fp32
- * and y is rounded once.  Any M, N >= 1; the kernel reads the weight once
- * per 64 tokens, so it is meant for M up to about that.  M = 0 enqueues
- * nothing.  No workspace; the same bits on every run.                       */
+ * and y is rounded once.  Codes are summed with an offset (bf16: 128), so y
+ * is not finite, and may be NaN where the product is an infinity, for a token
+ * whose x holds one, or whose sums of |x| times the row's largest |value|
+ * pass 2^120.  Any M, N >= 1; the kernel reads the weight once per 64 tokens,
+ * so it is meant for M up to about that.  M = 0 enqueues nothing.  No
+ * workspace; the same bits on every run.                                    */
 int qlora_linear_u4_fwd(const qlora_u4_weight* w, const uint16_t* x, int64_t ldx, int64_t M,
                         uint16_t* y, int64_t ldy, void* stream);
 int qlora_linear_u4_fwd_f16(const qlora_u4_weight* w, const uint16_t* x, int64_t ldx, int64_t M,
@@ -447,7 +450,8 @@ typedef struct qlora_kv4_cache {
  * block_table[b][p / page_size].  The arrays are device memory that the
  * host does not see; on the device,
  *   - rows past `rows` and beyond `max_q` of a sequence are not worked on,
- *     and rows behind cu_q[seqs] are left as they were;
+ *     nor is a sequence that starts before row 0 or behind its end, and rows
+ *     behind cu_q[seqs] are left as they were;
  *   - a position without a page (past the table, or an entry outside
  *     0 .. pages - 1, such as -1 for a page given back) is a token that is
  *     not there: not stored, not attended to, read as zeros;
@@ -478,7 +482,8 @@ typedef struct qlora_kv4_batch {
  *     rot is 0 (no rotation; cos_sin may be NULL) or a multiple of 8 up to
  *     head_dim (ESHAPE).
  *   q_out [rows, q_heads, head_dim], densely packed: the rotated queries,
- *     rounded once.  Keys are encoded from the unrounded rotation.
+ *     rounded to fp32 and then to 16 bits.  Keys are encoded from the
+ *     unrounded rotation.
  * A row at a negative position, or past the cos_sin table, stores nothing
  * and its q_out is NaN.  No workspace.                                      */
 int qlora_kv4_append(const qlora_kv4_cache* cache, const qlora_kv4_batch* batch, const uint16_t* k,
@@ -511,11 +516,16 @@ int qlora_kv4_read_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch* batc
  *     window > 0 those with j > p - window.
  *   max_len: at least the longest seq_lens (it sets how the keys are split
  *     over the chip and the workspace; a sequence that is longer all the
- *     same is attended in full, with larger shares).
+ *     same is attended in full, with larger shares).  The split takes every
+ *     sequence to have max_q rows: where a few have many more rows than the
+ *     others, a call for each kind is faster.
  *   out [rows, q_heads, head_dim], densely packed, rounded once from fp32;
  *   lse [rows, q_heads] fp32 (or NULL): the logarithm of the sum of
  *     exp(score).  A row that sees nothing gets zeros and -infinity.
  *   What a hidden token's memory holds, NaN included, has no effect.
+ *   Products are exact to fp32 but for the weights of the values' product,
+ *   which are fp16 (for fp16 outputs two of them): outputs are off by next to
+ *   nothing beside their own rounding, for values up to 2^100 in magnitude.
  * scale must be finite (EINVAL).  workspace (256-byte aligned): at least
  * qlora_kv4_attention_workspace_bytes(seqs, max_q, max_len, ...) bytes, or
  * NULL where that is 0 (also its answer for an invalid shape); it is written
