@@ -66,7 +66,7 @@ constexpr float kMid = 8.0f;
 // p s' is 2^kUp, 2^20 times the smallest normal fp16 number, and moves M again
 // when it would pass 2^kMost, inside fp16.  With small steps M stays at the
 // largest z log2 e less kUnder, so that sums of p stay inside fp32.
-constexpr float kUp = 6.0f, kMost = 14.0f, kUnder = 60.0f;
+constexpr float kUp = 6.0f, kMost = 14.0f, kUnder = 40.0f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(64 * kWaves, D * NT >= 256 ? 2 : 3) void kv4_attent
         const float to = fmaxf(ceilf(r) - kUp, ceilf(top) - kUnder);
         const float f = !move                  ? 1.0f
                         : gate[n] == -INFINITY ? 0.0f
-                                               : __builtin_amdgcn_exp2f(mu[n] - to);
+                                               : exp2f(mu[n] - to);
         mu[n] = move ? to : mu[n];
         gate[n] = move ? to + kMost : gate[n];
 #pragma unroll

@@ -525,7 +525,8 @@ int qlora_kv4_read_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch* batc
  *   What a hidden token's memory holds, NaN included, has no effect.
  *   Products are exact to fp32 but for the weights of the values' product,
  *   which are fp16 (for fp16 outputs two of them): outputs are off by next to
- *   nothing beside their own rounding, for values up to 2^100 in magnitude.
+ *   nothing beside their own rounding, for values of 0 and of 2^-50 to 2^100 in
+ *   magnitude (between 2^-50 and 0 they lose bits).
  * scale must be finite (EINVAL).  workspace (256-byte aligned): at least
  * qlora_kv4_attention_workspace_bytes(seqs, max_q, max_len, ...) bytes, or
  * NULL where that is 0 (also its answer for an invalid shape); it is written

@@ -169,3 +169,24 @@ def test_scores_and_steps_against_each_other(cuda, D):
             ro, _ = ref.outputs(pool, f64(qq), [1], SCALE[D])
             check_norm(f"D{D} {sign}", f64(out.t), ro, "bf16")
             ref.check_lse(pool, f64(qq), f64(lse.t), [1], SCALE[D])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("at", [0, 150, 700, 1099])
+@pytest.mark.parametrize("size", [20, 60, 95])
+def test_large_values_among_constant_ones(cuda, D, at, size):
+    """Tokens without a spread (s = 0, values 0 or 1) and one whose values are
+    2^size: it is weighted as the others are."""
+    for rest in (0.0, 1.0):
+        pool = steps_pool(lambda t: np.where(t == at, 2.0 ** size, 0.0), [1100], D)
+        x = np.full((1100, 1, D), rest)
+        x[at] = pool.rng.standard_normal((1, D)) * 2.0 ** size
+        c, p = u4.encode(x)
+        for t in range(1100):
+            where = pool.table[0, t // 16], slice(None), t % 16
+            pool.codes["v"][where], pool.pairs["v"][where] = u4.pack(c[t]), p[t]
+        for max_len in (1100, 0):              # chunks of 256, and one
+            qv, o, lse = attend(pool, [2], 2, "bf16", causal=False, max_len=max_len)
+            ro, _ = ref.outputs(pool, qv, [2], SCALE[D], causal=False)
+            check_norm(f"D{D} {at} 2^{size} {rest}", o, ro, "bf16")
+            ref.check_lse(pool, qv, lse, [2], SCALE[D], causal=False)
