@@ -42,10 +42,14 @@ from ._lib import (  # noqa: F401
     workspace_bytes,
 )
 
-# The 4-bit serving calls live in ``u4``, which needs torch; the rest of the
-# package does without until a call is made, so they are imported on first use.
+# The serving calls live in ``u4`` (4 bits) and ``i8`` (8 bits), which need
+# torch; the rest of the package does without until a call is made, so they are
+# imported on first use.
 _U4 = ("Kv4Cache", "U4Weight", "dequantize_u4", "kv4_append", "kv4_attention",
        "kv4_attention_workspace_bytes", "kv4_read", "linear_u4_fwd", "quantize_u4")
+_I8 = ("I8Tokens", "I8Weight", "dequantize_i8", "dequantize_tokens_i8", "gated_i8_fwd",
+       "linear_i8_fwd", "linear_i8_workspace_bytes", "quantize_i8", "quantize_tokens_i8",
+       "rms_norm_i8")
 
 
 def __getattr__(name):
@@ -53,5 +57,10 @@ def __getattr__(name):
         from . import u4
         for n in _U4:
             globals()[n] = getattr(u4, n)
+        return globals()[name]
+    if name in _I8:
+        from . import i8
+        for n in _I8:
+            globals()[n] = getattr(i8, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -37,7 +37,13 @@ EXPORTS = ("qlora_quantize_nf4", "qlora_double_quant", "qlora_quantize_nf4_dq",
            "qlora_linear_u4_fwd", "qlora_linear_u4_fwd_f16",
            "qlora_kv4_append", "qlora_kv4_append_f16", "qlora_kv4_read", "qlora_kv4_read_f16",
            "qlora_kv4_attention_workspace_bytes", "qlora_kv4_attention",
-           "qlora_kv4_attention_f16")
+           "qlora_kv4_attention_f16",
+           "qlora_quantize_i8", "qlora_dequantize_i8", "qlora_dequantize_i8_f16",
+           "qlora_quantize_tokens_i8", "qlora_quantize_tokens_i8_f16",
+           "qlora_dequantize_tokens_i8", "qlora_dequantize_tokens_i8_f16",
+           "qlora_rms_norm_i8", "qlora_rms_norm_i8_f16", "qlora_linear_i8_workspace_bytes",
+           "qlora_linear_i8_fwd", "qlora_linear_i8_fwd_f16",
+           "qlora_gated_i8_fwd", "qlora_gated_i8_fwd_f16")
 
 
 class QloraError(RuntimeError):
@@ -77,6 +83,18 @@ class Kv4BatchStruct(ctypes.Structure):
                 ("max_q", ctypes.c_int32)]
 
 
+class I8WeightStruct(ctypes.Structure):
+    """``qlora_i8_weight``."""
+    _fields_ = [("tiles", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64)]
+
+
+class I8TokensStruct(ctypes.Structure):
+    """``qlora_i8_tokens``."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("M", ctypes.c_int64),
+                ("K", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -95,6 +113,12 @@ def lib() -> ctypes.CDLL:
     up, cp, bp = (ctypes.POINTER(U4Struct), ctypes.POINTER(Kv4CacheStruct),
                   ctypes.POINTER(Kv4BatchStruct))
     append = [cp, bp, vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, vp, i64, i32, i32, vp, vp]
+    iw, it, f64 = (ctypes.POINTER(I8WeightStruct), ctypes.POINTER(I8TokensStruct),
+                   ctypes.c_double)
+    tokens = [vp, i64, i64, i64, vp, vp, vp]
+    norm = [vp, i64, vp, i64, vp, f64, i64, i64, vp, i64, vp, vp, vp]
+    product = [iw, it, vp, i64, vp, sz, vp]
+    gated = [iw, iw, i32, it, vp, i64, vp, sz, vp]
     attend = [cp, bp, vp, i64, i64, i32, f32, i32, i32, i64, vp, vp, vp, sz, vp]
     sig = {
         "qlora_quantize_nf4": ([vp, i64, i32, vp, vp, vp], ctypes.c_int),
@@ -143,6 +167,20 @@ def lib() -> ctypes.CDLL:
         "qlora_kv4_attention_workspace_bytes": ([i64, i64, i64, i32, i32, i32, i32], sz),
         "qlora_kv4_attention": (attend, ctypes.c_int),
         "qlora_kv4_attention_f16": (attend, ctypes.c_int),
+        "qlora_quantize_i8": ([vp, i64, i64, vp, vp, vp], ctypes.c_int),
+        "qlora_dequantize_i8": ([iw, vp, vp], ctypes.c_int),
+        "qlora_dequantize_i8_f16": ([iw, vp, vp], ctypes.c_int),
+        "qlora_quantize_tokens_i8": (tokens, ctypes.c_int),
+        "qlora_quantize_tokens_i8_f16": (tokens, ctypes.c_int),
+        "qlora_dequantize_tokens_i8": ([it, vp, vp], ctypes.c_int),
+        "qlora_dequantize_tokens_i8_f16": ([it, vp, vp], ctypes.c_int),
+        "qlora_rms_norm_i8": (norm, ctypes.c_int),
+        "qlora_rms_norm_i8_f16": (norm, ctypes.c_int),
+        "qlora_linear_i8_workspace_bytes": ([i64, i64, i64, i32], sz),
+        "qlora_linear_i8_fwd": (product, ctypes.c_int),
+        "qlora_linear_i8_fwd_f16": (product, ctypes.c_int),
+        "qlora_gated_i8_fwd": (gated, ctypes.c_int),
+        "qlora_gated_i8_fwd_f16": (gated, ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -574,13 +612,14 @@ def merge_adapter(base, A, B, alpha: float, out_f32: bool = True, out_bf16: bool
     """W_m = W_base + (alpha/r).B.A for export.  ``base`` is a PackedWeight
     (merge into the decoded 4-bit base) or an fp32 [N, K] device tensor (the
     original weights).  Returns ``(fp32 [N, K] or None, bf16 bits [N, K]
-    (int16) or None, PackedWeight, U4Weight or None)``; the last is the fp32
-    merge quantised again (needs the fp32 output): to NF4 with
+    (int16) or None, PackedWeight, U4Weight, I8Weight or None)``; the last is
+    the fp32 merge quantised again (needs the fp32 output): to NF4 with
     ``requantize=True`` or ``"nf4"``, to the 4-bit group format (groups of 64)
-    with ``requantize="u4"``; other texts are refused."""
+    with ``requantize="u4"``, to the 8-bit row format with
+    ``requantize="i8"``; other texts are refused."""
     torch = _torch()
-    if isinstance(requantize, str) and requantize not in ("", "nf4", "u4"):
-        raise ValueError(f"requantize: True, False, 'nf4' or 'u4', not {requantize!r}")
+    if isinstance(requantize, str) and requantize not in ("", "nf4", "u4", "i8"):
+        raise ValueError(f"requantize: True, False, 'nf4', 'u4' or 'i8', not {requantize!r}")
     if requantize and not out_f32:
         raise ValueError("requantize needs the fp32 merge")
     packed = isinstance(base, PackedWeight)
@@ -600,5 +639,8 @@ def merge_adapter(base, A, B, alpha: float, out_f32: bool = True, out_bf16: bool
     if requantize == "u4":
         from .u4 import quantize_u4
         return f, b, quantize_u4(f)
+    if requantize == "i8":
+        from .i8 import quantize_i8
+        return f, b, quantize_i8(f)
     q = quantize_weight(f) if requantize else None
     return f, b, q

@@ -1,0 +1,117 @@
+// A weight in the 8-bit row format and its tiles (i8_common.h): the quantiser
+// of fp32 rows and what they stand for.
+//
+// A block of sixteen waves has a panel of 16 rows, a wave a row.  The row is
+// read twice, for its largest magnitude and for its codes.  Codes
+// of 1024 columns of the panel go through LDS into the tiles' order, which is
+// one run of 16 KiB, so every store is whole lines.
+
+#include "i8_common.h"
+#include "launch.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kCols = 1024;         // columns of a panel at a time
+constexpr int kLdsRow = kCols + 16;  // bytes: the rows' pieces in different banks
+
+__device__ __forceinline__ f32x4_t load4(const float* p, int64_t k, int64_t K) {
+  f32x4_t v = {0, 0, 0, 0};
+  if (k + 4 <= K) {
+    __builtin_memcpy(&v, p + k, 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k + j < K) v[j] = p[k + j];
+  }
+  return v;
+}
+
+__global__ __launch_bounds__(1024) void quantize_i8_kernel(const float* __restrict__ w, int64_t N,
+                                                           int64_t K, int8_t* __restrict__ tiles,
+                                                           float* __restrict__ scales) {
+  __shared__ __attribute__((aligned(16))) int8_t lds[16 * kLdsRow];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 16 + wave, Kp = i8_padded(K);
+  const bool row = n < N;
+  const float* src = w + (row ? n : 0) * K;
+  uint32_t top = 0;
+  if (row)
+    for (int64_t k = 4 * lane; k < K; k += 256) {
+      const f32x4_t v = load4(src, k, K);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    }
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+  const I8Row code = i8_row(__uint_as_float(top), 1.0, top < 0x7F800000u);
+  if (row && lane == 0) scales[n] = code.s;
+  int8_t* dst = tiles + (int64_t)blockIdx.x * 16 * Kp;
+  for (int64_t k0 = 0; k0 < Kp; k0 += kCols) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t k = k0 + 256 * i + 4 * lane;
+      uint32_t c = 0;
+      if (row && k < K) {
+        const f32x4_t v = load4(src, k, K);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c |= ((uint32_t)i8_code(code, v[j]) & 0xFFu) << (8 * j);
+      }
+      *reinterpret_cast<uint32_t*>(&lds[wave * kLdsRow + 256 * i + 4 * lane]) = c;
+    }
+    __syncthreads();
+    // thread t has piece (t % 64) / 16 of row t % 16 of tile t / 64
+    const int t = threadIdx.x, col = 64 * (t >> 6) + 16 * ((t >> 4) & 3);
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(&lds[(t & 15) * kLdsRow + col]);
+    if (k0 + col < Kp) *reinterpret_cast<u32x4_t*>(dst + 16 * k0 + 16 * t) = v;
+    __syncthreads();
+  }
+}
+
+// A wave has a row of the panel, a lane 16 columns of it: the sixteen waves
+// read the lines of a tile together.
+template <class DT>
+__global__ __launch_bounds__(1024) void dequantize_i8_kernel(const int8_t* __restrict__ tiles,
+                                                             const float* __restrict__ scales,
+                                                             int64_t N, int64_t K,
+                                                             uint16_t* __restrict__ out) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 16 + wave, Kp = i8_padded(K);
+  if (n >= N) return;
+  const float s = scales[n];
+  const int8_t* src = tiles + (int64_t)blockIdx.x * 16 * Kp + 16 * wave;
+  for (int64_t k = 16 * lane; k < K; k += kCols) {
+    const u32x4_t c =
+        *reinterpret_cast<const u32x4_t*>(src + (k >> 6) * kI8Tile + ((k >> 4) & 3) * 256);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      u32x4_t v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t b = c[2 * q + j / 2] >> (16 * (j & 1));
+        v[j] = DT::pack2(i8_value((int8_t)b, s), i8_value((int8_t)(b >> 8), s));
+      }
+      if (k + 8 * q < K) store_piece(out + n * K, (int)k + 8 * q, (int)K, v);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_quantize_i8(const float* w, int64_t N, int64_t K, int8_t* tiles, float* scales,
+                              hipStream_t s) {
+  quantize_i8_kernel<<<dim3((unsigned)((N + 15) / 16)), 1024, 0, s>>>(w, N, K, tiles, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_dequantize_i8(const int8_t* tiles, const float* scales, int64_t N, int64_t K,
+                                uint16_t* out, bool f16, hipStream_t s) {
+  const dim3 grid((unsigned)((N + 15) / 16));
+  if (f16)
+    dequantize_i8_kernel<F16T><<<grid, 1024, 0, s>>>(tiles, scales, N, K, out);
+  else
+    dequantize_i8_kernel<Bf16T><<<grid, 1024, 0, s>>>(tiles, scales, N, K, out);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

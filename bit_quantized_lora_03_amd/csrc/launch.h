@@ -251,4 +251,41 @@ size_t kv4_attn_workspace(const Kv4AttnPlan& p, int64_t seqs, int kv_heads, int 
 hipError_t launch_kv4_attention(const Kv4CacheArg& c, const Kv4BatchArg& b, const Kv4AttnArg& a,
                                 const Kv4AttnPlan& p, float* workspace, bool f16, hipStream_t s);
 
+// i8_rows.hip, i8_weight.hip -- the 8-bit row format (i8_common.h): one fp32
+// scale a row, K padded to 128 columns; a weight in tiles of 16 rows and 64
+// columns.
+struct I8RowsArg {
+  const uint16_t* x;    // [M, K], rows ldx apart
+  const uint16_t* res;  // added to x, or null
+  const uint16_t* w;    // [K]: the norm's weight; null: x itself is coded
+  uint16_t* h;          // [M, K], rows ldh apart: x + res (with res only); may
+                        // be x or res
+  int64_t ldx, ldr, ldh, M, K;
+  double eps;
+  int8_t* codes;  // [M, K padded]
+  float* scales;  // [M]
+};
+hipError_t launch_rows_i8(const I8RowsArg& p, bool f16, hipStream_t s);
+hipError_t launch_values_i8(const int8_t* codes, const float* scales, int64_t M, int64_t K,
+                            uint16_t* out, bool f16, hipStream_t s);
+hipError_t launch_quantize_i8(const float* w, int64_t N, int64_t K, int8_t* tiles, float* scales,
+                              hipStream_t s);
+hipError_t launch_dequantize_i8(const int8_t* tiles, const float* scales, int64_t N, int64_t K,
+                                uint16_t* out, bool f16, hipStream_t s);
+
+// i8_linear.hip -- y = x . W^T of 8-bit tokens and weights, or with a second
+// weight act(x . W^T) * (x . U^T)
+struct I8LinearArg {
+  const int8_t* tiles[2];  // the second null for a plain product
+  const float* wscale[2];
+  const int8_t* codes;  // [M, K padded]
+  const float* xscale;
+  uint16_t* y;
+  int64_t ldy, M, N, K;
+  int act;  // kI8Silu, kI8Gelu
+};
+constexpr int kI8Silu = 0, kI8Gelu = 1;
+size_t linear_i8_workspace(int64_t M, int64_t N, int64_t K, bool gated);
+hipError_t launch_linear_i8(const I8LinearArg& p, int32_t* workspace, bool f16, hipStream_t s);
+
 }  // namespace qlora

@@ -546,6 +546,108 @@ int qlora_kv4_attention_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch*
                             uint16_t* out, float* lse, void* workspace, size_t ws_bytes,
                             void* stream);
 
+/* ---- 8-bit serving: row format, norm, products ----------------------------
+ * What the prompts of a served model need: where many tokens meet a weight,
+ * the matrix cores bound the product, and 8-bit integers take half the time
+ * of 16-bit floats.  The pages give no such format; it is this library's
+ * reading.
+ *
+ * The 8-bit row format.  A row (a token, or an output channel of a weight)
+ * has one fp32 scale s and an int8 code c for each value; a value is s * c.
+ *   Encoding: a = the row's largest magnitude, s = fp32(a / 127),
+ *   c = rint(127 v / a), the exact quotient, half to even (0 where a is 0).
+ *   So |c| <= 127 and |value - v| <= a / 254 but for the rounding of s.
+ *   A row that holds a NaN or an infinity, or whose scale is none in fp32,
+ *   gets s = NaN and codes 0: everything that is computed from it is NaN.
+ * Tokens are rows in memory, K rounded up to a multiple of 128 columns.  A
+ * weight is in tiles of 16 rows and 64 columns, in the order in which the
+ * matrix instructions read them: element (n, k) of W [N, K] is byte
+ *   ((n / 16) * (Kp / 64) + k / 64) * 1024 + (k % 64) / 16 * 256
+ *     + (n % 16) * 16 + k % 16,               Kp = K rounded up to 128,
+ * and N is rounded up to 16.  Codes of columns from K on have to be 0 in
+ * both, as the quantisers write them (rows of a weight from N on may hold
+ * anything).
+ * Codes are 16-byte, scales 4-byte, 16-bit tensors and fp32 weights element
+ * aligned (EALIGN).  No output may overlap an input or another output
+ * (EINVAL) but where said so; of strided tensors that is the range from the
+ * first to the last element, gaps included.  K is 1 .. 2^17 - 128, N
+ * 1 .. 2^26 - 16, M 0 .. 2^30 (ESHAPE); M = 0 enqueues nothing.             */
+typedef struct qlora_i8_weight {
+  const int8_t* tiles;   /* [ceil(N/16)][Kp/64][4][16][16] */
+  const float*  scales;  /* [N]                            */
+  int64_t       N;
+  int64_t       K;
+} qlora_i8_weight;
+typedef struct qlora_i8_tokens {
+  const int8_t* codes;   /* [M, Kp] */
+  const float*  scales;  /* [M]     */
+  int64_t       M;
+  int64_t       K;
+} qlora_i8_tokens;
+
+/* fp32 w [N, K] to tiles and scales, and back: out [N, K] = s * c rounded to
+ * fp32 and then to bf16 (_f16: fp16).                                       */
+int qlora_quantize_i8(const float* w, int64_t N, int64_t K, int8_t* tiles, float* scales,
+                      void* stream);
+int qlora_dequantize_i8(const qlora_i8_weight* w, uint16_t* out, void* stream);
+int qlora_dequantize_i8_f16(const qlora_i8_weight* w, uint16_t* out, void* stream);
+
+/* x [M, K] bf16 (_f16: fp16), rows ldx >= K elements apart, to codes [M, Kp]
+ * and scales [M], and back: out [M, K], densely packed.                     */
+int qlora_quantize_tokens_i8(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, int8_t* codes,
+                             float* scales, void* stream);
+int qlora_quantize_tokens_i8_f16(const uint16_t* x, int64_t ldx, int64_t M, int64_t K,
+                                 int8_t* codes, float* scales, void* stream);
+int qlora_dequantize_tokens_i8(const qlora_i8_tokens* t, uint16_t* out, void* stream);
+int qlora_dequantize_tokens_i8_f16(const qlora_i8_tokens* t, uint16_t* out, void* stream);
+
+/* Root-mean-square norm of a residual stream, written as 8-bit tokens:
+ *   h = x + residual, rounded to fp32 and then to 16 bits (h = x where
+ *       residual is NULL);
+ *   codes and scales of the rows h * weight / sqrt(mean(h^2) + eps).
+ *   x, residual, h [M, K] bf16 (_f16: fp16), rows ldx, ldr, ldh >= K apart;
+ *   weight [K] of the same type.  h is written where residual is given and
+ *   has to be NULL otherwise (EINVAL); it may be x or residual itself (the
+ *   same address and row distance), no other overlap.
+ *   eps >= 0 and finite (EINVAL).  Sums, products and quotients are fp64.
+ * A row of zeros has scale 0 with any eps > 0, and NaN with eps = 0.        */
+int qlora_rms_norm_i8(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
+                      const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* h,
+                      int64_t ldh, int8_t* codes, float* scales, void* stream);
+int qlora_rms_norm_i8_f16(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
+                          const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* h,
+                          int64_t ldh, int8_t* codes, float* scales, void* stream);
+
+/* y = x . W^T, [M, N] bf16 (_f16: fp16), rows ldy >= N elements apart; x->K
+ * has to be w->K (EINVAL).  The sums of the codes' products are exact (int32);
+ * y = sum * sw[n] * sx[m] in fp32, left to right, rounded once to 16 bits.
+ * The same bits on every run and for every M.  M up to 2^20 - 16, and M * N
+ * up to 2^34 (ESHAPE).
+ * workspace (256-byte aligned): at least
+ * qlora_linear_i8_workspace_bytes(M, N, K, 0) bytes, or NULL where that is 0
+ * (also its answer for an invalid shape); it is written before it is read.  */
+size_t qlora_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t gated);
+int qlora_linear_i8_fwd(const qlora_i8_weight* w, const qlora_i8_tokens* x, uint16_t* y,
+                        int64_t ldy, void* workspace, size_t ws_bytes, void* stream);
+int qlora_linear_i8_fwd_f16(const qlora_i8_weight* w, const qlora_i8_tokens* x, uint16_t* y,
+                            int64_t ldy, void* workspace, size_t ws_bytes, void* stream);
+
+/* The gated half of an MLP: y = act(g) * u with g = x . gate^T and
+ * u = x . up^T (weights of one shape, EINVAL), in one pass; g and u are fp32
+ * and never rounded to 16 bits.  act (ENOTSUP for others):
+ *   QLORA_ACT_SILU  g / (1 + exp(-g))
+ *   QLORA_ACT_GELU  the tanh form, g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
+ * Other arguments as above; workspace
+ * qlora_linear_i8_workspace_bytes(M, N, K, 1).                              */
+#define QLORA_ACT_SILU 0
+#define QLORA_ACT_GELU 1
+int qlora_gated_i8_fwd(const qlora_i8_weight* gate, const qlora_i8_weight* up, int32_t act,
+                       const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* workspace,
+                       size_t ws_bytes, void* stream);
+int qlora_gated_i8_fwd_f16(const qlora_i8_weight* gate, const qlora_i8_weight* up, int32_t act,
+                           const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* workspace,
+                           size_t ws_bytes, void* stream);
+
 /* Workspace bytes for op 0 (forward) or 1 (backward) of the NF4 layer,
  * op 2 (forward) or 3 (backward) of the bf16-weight layer, op 4 (forward)
  * or 5 (backward) of the NF4 layer with dropout, op 6 (forward) or 7

@@ -1,0 +1,636 @@
+"""GPU parity of the 8-bit row format, its products and the norm that writes it
+against the fp64 oracle.
+
+Bars.  Codes are compared value for value: the kernels decide borders as the
+exact quotient does.  A scale is fp32(a / 127), bit for bit; a norm's has an
+fp64 root whose sum the kernel adds in another order (2^-45 at most for these
+rows), so it may fall on the other side of a border of fp32: one step, 2^-23.
+What a code stands for is s c rounded to fp32 and then to 16 bits, bit for bit.
+
+The product's sums are exact integers, so y is fp32(sum), times sw, times sx,
+each rounded to fp32, then to 16 bits: bit for bit again.
+
+The gated product: g and u have three roundings to fp32, 3 2^-24 of
+themselves.  act(g) = g / (1 + e), e = exp(-z): its slope is at most 1.13, so
+g's roundings move it by 1.13 * 3 2^-24 |g|; e has the relative error of its
+exponent, at most 2^-22 (1 + |z|) with z's own roundings (gelu: z = 1.6 g +
+0.07 g^3 has six roundings and g's three up to threefold, 15 2^-24 |z|, so
+2^-20 (1 + |z|) covers both forms); the sum, the reciprocal (an ulp) and two
+products add 5 2^-24.  Times u and rounded to 16 bits:
+  |y - ref| <= u16 |ref| + |act u| 2^-20 (3 + |z|) + 2^-21 |g u| + tiny,
+tiny = half a step of fp16's subnormals (2^-25), and |g u| 2^-120 where e
+passes fp32's range."""
+
+import numpy as np
+import pytest
+
+import bit_quantized_lora_03_amd as q
+from oracle import i8
+from tests.gpu_util import Guarded
+
+pytestmark = pytest.mark.gpu
+
+U16 = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TYPES = pytest.mark.parametrize("dtype", ["bf16", "f16"])
+
+
+def tdtype(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f16": torch.float16}[name]
+
+
+def bits(t):
+    import torch
+    return t.detach().contiguous().view(torch.int16).cpu().numpy()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def round16(a32, dtype):
+    """fp32 numpy -> 16-bit patterns, nearest even."""
+    import torch
+    return bits(torch.from_numpy(np.ascontiguousarray(a32, dtype=np.float32)).to(tdtype(dtype)))
+
+
+def activations(M, K, dtype, seed, spread=0.5):
+    """16-bit rows as torch holds them, on the GPU, and in fp64."""
+    import torch
+    rng = np.random.default_rng(seed)
+    v = rng.standard_normal((M, K)) * np.exp(spread * rng.standard_normal(K))
+    t = torch.from_numpy(v.astype(np.float32)).to(tdtype(dtype)).cuda()
+    return t, f64(t)
+
+
+def weights(N, K, seed):
+    return (np.random.default_rng(seed).standard_normal((N, K)) * 0.02).astype(np.float32)
+
+
+def i8_weight(w):
+    """The oracle's coding of w on the GPU, and its codes and scales."""
+    c, s = i8.encode(w)
+    return q.I8Weight(dev(i8.tile(c)), dev(s), *w.shape), c, s
+
+
+def i8_tokens(M, K, seed):
+    rng = np.random.default_rng(seed)
+    c, s = i8.encode(rng.standard_normal((M, K)) * np.exp(0.5 * rng.standard_normal(K)))
+    return q.I8Tokens(dev(i8.pad(c)), dev(s), K), c, s
+
+
+def scaled(sums, sw, sx):
+    """fp32(sum) sw sx as the library rounds it."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        return (sums.astype(np.float32) * sw) * sx[:, None]
+
+
+# ---------------------------------------------------------------------------
+# weights
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("N,K", [(1, 1), (1, 128), (3, 127), (16, 64), (17, 129), (40, 1000),
+                                 (33, 1025), (100, 4097), (256, 2048)])
+def test_quantize_weight(cuda, N, K):
+    w = weights(N, K, N + K)
+    w[0, :] = np.float32(0.25) * (np.arange(K) % 3 - 1)
+    if N > 2:
+        w[1] = 0.0
+        w[2] = np.random.default_rng(K).integers(-254, 255, K) * 0.5     # halves of codes
+        w[2, 0] = 127.0
+    iw = q.quantize_i8(dev(w))
+    c, s = i8.encode(w)
+    assert np.array_equal(iw.tiles.cpu().numpy(), i8.tile(c))
+    assert np.array_equal(iw.scales.cpu().numpy().view(np.uint32), s.view(np.uint32))
+    for dtype in ("bf16", "f16"):
+        got = bits(q.dequantize_i8(iw, tdtype(dtype)))
+        assert np.array_equal(got, round16(c.astype(np.float32) * s[:, None], dtype))
+
+
+def test_quantize_weight_scales_and_special_rows(cuda):
+    rng = np.random.default_rng(1)
+    w = rng.standard_normal((60, 300)).astype(np.float32)
+    for i, e in enumerate((-148, -140, -127, -100, -30, 30, 100, 126)):
+        w[3 + i] = np.ldexp(w[3 + i].astype(np.float64) / 4, e).astype(np.float32)
+    w[20, 7], w[21, 299], w[22, 0], w[23] = np.nan, np.inf, -np.inf, np.nan
+    w[24, 3], w[25] = 3.4028235e38, -3.4028235e38
+    c, s = i8.encode(w)
+    iw = q.quantize_i8(dev(w))
+    assert np.array_equal(iw.tiles.cpu().numpy(), i8.tile(c))
+    got = iw.scales.cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(s)) and np.isnan(s).sum() == 4
+    assert np.array_equal(got[~np.isnan(s)], s[~np.isnan(s)])
+
+
+def test_quantize_weight_writes_nothing_else(cuda):
+    import torch
+    N, K = 37, 333
+    w = dev(weights(N, K, 0))
+    tiles, scales = Guarded((3, 6, 4, 16, 16), torch.int8), Guarded((N,), torch.float32)
+    assert q.lib().qlora_quantize_i8(w.data_ptr(), N, K, tiles.t.data_ptr(), scales.t.data_ptr(),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+    tiles.check("tiles")
+    scales.check("scales")
+    c, s = i8.encode(w.cpu().numpy())
+    assert np.array_equal(tiles.t.cpu().numpy(), i8.tile(c))
+    assert np.array_equal(scales.t.cpu().numpy(), s)
+
+
+# ---------------------------------------------------------------------------
+# tokens
+# ---------------------------------------------------------------------------
+
+WIDTHS = [1, 7, 8, 127, 128, 129, 500, 512, 513, 1024, 2048, 2056, 4096, 4097, 8192, 11008, 16384,
+          16392, 22016, 32768, 40001, 65544, 130944]
+
+
+@TYPES
+@pytest.mark.parametrize("K", WIDTHS)
+def test_quantize_tokens(cuda, K, dtype):
+    for M in (1, 6):
+        x, v = activations(M, K, dtype, K + M)
+        t = q.quantize_tokens_i8(x)
+        c, s = i8.encode(v)
+        assert np.array_equal(t.codes.cpu().numpy(), i8.pad(c))
+        assert np.array_equal(t.scales.cpu().numpy(), s)
+        for out in ("bf16", "f16"):
+            got = bits(q.dequantize_tokens_i8(t, tdtype(out)))
+            assert np.array_equal(got, round16(c.astype(np.float32) * s[:, None], out))
+
+
+@TYPES
+def test_quantize_tokens_special_rows(cuda, dtype):
+    import torch
+    x, _ = activations(12, 700, dtype, 3)
+    x[1] = 0.0
+    x[2, 699], x[3, 0], x[4, 350] = float("nan"), float("inf"), -float("inf")
+    x[5] = torch.finfo(x.dtype).max
+    x[6] = -torch.finfo(x.dtype).smallest_normal
+    x[7] = torch.finfo(x.dtype).smallest_normal / 4         # subnormal
+    x[8] = torch.arange(700, device="cuda") % 255 * 0.5       # halves of codes
+    x[8, 0] = 127.0
+    x[9] = -0.0
+    c, s = i8.encode(f64(x))
+    t = q.quantize_tokens_i8(x)
+    got = t.scales.cpu().numpy()
+    assert np.array_equal(t.codes.cpu().numpy(), i8.pad(c))
+    assert np.array_equal(np.isnan(got), np.isnan(s)) and np.isnan(s).sum() == 3
+    assert np.array_equal(got[~np.isnan(s)], s[~np.isnan(s)])
+
+
+@TYPES
+@pytest.mark.parametrize("K,left,right", [(300, 8, 20), (256, 1, 0), (2055, 3, 4), (4096, 0, 5)])
+def test_strided_rows_and_guards(cuda, K, left, right, dtype):
+    """Rows that start anywhere; nothing behind them is read as theirs."""
+    import torch
+    M = 9
+    wide, _ = activations(M, left + K + right, dtype, K)
+    wide[:, :left] = float("nan")
+    wide[:, left + K:] = float("inf")
+    x = wide[:, left:left + K]
+    c, s = i8.encode(f64(x))
+    codes = Guarded((M, i8.padded(K)), torch.int8)
+    scales = Guarded((M,), torch.float32)
+    out = q.I8Tokens(codes.t, scales.t, K)
+    assert q.quantize_tokens_i8(x, out=out) is out
+    codes.check("codes")
+    scales.check("scales")
+    assert np.array_equal(codes.t.cpu().numpy(), i8.pad(c))
+    assert np.array_equal(scales.t.cpu().numpy(), s)
+    # every other row
+    c2, s2 = i8.encode(f64(x[::2]))
+    t = q.quantize_tokens_i8(x[::2])
+    assert np.array_equal(t.codes.cpu().numpy(), i8.pad(c2)) and np.array_equal(t.scales.cpu().numpy(), s2)
+
+
+# ---------------------------------------------------------------------------
+# the norm
+# ---------------------------------------------------------------------------
+
+def check_norm(t, h, weight, eps):
+    """tokens t of the rows h (fp64, as stored)."""
+    c, s = i8.norm(h, weight, eps)
+    got = t.scales.cpu().numpy()
+    assert np.array_equal(t.codes.cpu().numpy(), i8.pad(c))
+    assert np.array_equal(np.isnan(got), np.isnan(s))
+    ok = ~np.isnan(s)
+    assert np.all(np.abs(got[ok].astype(np.float64) - s[ok]) <= 2.0 ** -23 * s[ok])
+
+
+@TYPES
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("K", WIDTHS)
+def test_norm(cuda, K, residual, dtype):
+    for M, eps in ((1, 1e-5), (5, 0.3)):
+        x, v = activations(M, K, dtype, K)
+        r = activations(M, K, dtype, K + 1)[0] if residual else None
+        w = (1 + 0.1 * activations(1, K, dtype, 9)[0])[0].contiguous()
+        t, h = q.rms_norm_i8(x, w, eps, residual=r)
+        if residual:
+            want = (x.float() + r.float()).to(x.dtype)
+            assert np.array_equal(bits(h), bits(want))
+        else:
+            assert h is x
+        check_norm(t, f64(h), f64(w), eps)
+
+
+@TYPES
+def test_norm_special_rows(cuda, dtype):
+    """Zeros, infinities, NaN, and rows whose squares fp32 does not hold."""
+    import torch
+    M, K = 11, 900
+    x, _ = activations(M, K, dtype, 4)
+    big = torch.finfo(x.dtype).max
+    x[1] = 0.0
+    x[2, 3], x[3, 0], x[4, 899] = float("nan"), float("inf"), -float("inf")
+    x[5] = big
+    x[6] = torch.finfo(x.dtype).smallest_normal
+    x[7, ::2] = -big / 4
+    w = (1 + 0.1 * activations(1, K, dtype, 5)[0])[0].contiguous()
+    for eps in (1e-6, 1e30):
+        t, _ = q.rms_norm_i8(x, w, eps)
+        check_norm(t, f64(x), f64(w), eps)
+        assert np.isnan(t.scales.cpu().numpy()).sum() == 3 and t.scales[1] == 0
+    # without eps a row of zeros has no norm
+    t, _ = q.rms_norm_i8(x, w, 0.0)
+    check_norm(t, f64(x), f64(w), 0.0)
+    assert torch.isnan(t.scales[1])
+    # the sum of stream and addend may pass the type's range
+    t, h = q.rms_norm_i8(x, w, 1e-6, residual=x)
+    check_norm(t, f64(h), f64(w), 1e-6)
+    assert torch.isinf(h[5]).all()
+    # weights: a NaN or an infinity reaches every row, zeros none
+    for bad, none in ((float("nan"), True), (float("inf"), True), (0.0, False)):
+        w2 = w.clone()
+        w2[17] = bad
+        t, _ = q.rms_norm_i8(x[8:], w2, 1e-6)
+        assert torch.isnan(t.scales).all() == none
+        check_norm(t, f64(x[8:]), f64(w2), 1e-6)
+
+
+@TYPES
+@pytest.mark.parametrize("K", [129, 2048, 4100])
+def test_norm_in_place_and_strided(cuda, K, dtype):
+    import torch
+    M = 7
+    w = (1 + 0.1 * activations(1, K, dtype, 9)[0])[0].contiguous()
+    x, _ = activations(M, K + 11, dtype, 1)
+    r, _ = activations(M, K + 5, dtype, 2)
+    want = (x[:, 3:3 + K].float() + r[:, 1:1 + K].float()).to(x.dtype)
+    for place in ("x", "residual", "other"):
+        xs, rs = x.clone(), r.clone()
+        other = torch.full((M, K + 9), 7.0, dtype=x.dtype, device="cuda")
+        xv, rv = xs[:, 3:3 + K], rs[:, 1:1 + K]
+        h = {"x": xv, "residual": rv, "other": other[:, 2:2 + K]}[place]
+        t, got = q.rms_norm_i8(xv, w, 1e-5, residual=rv, h=h)
+        assert got is h and np.array_equal(bits(h), bits(want))
+        check_norm(t, f64(want), f64(w), 1e-5)
+        # what lies around is as it was
+        for now, was, a, name in ((xs, x, 3, "x"), (rs, r, 1, "residual")):
+            assert np.array_equal(bits(now[:, :a]), bits(was[:, :a]))
+            assert np.array_equal(bits(now[:, a + K:]), bits(was[:, a + K:]))
+            if place != name:
+                assert np.array_equal(bits(now), bits(was))
+        assert (other[:, :2] == 7).all() and (other[:, 2 + K:] == 7).all()
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+
+SHAPES = [(1, 1, 1), (1, 16, 128), (1, 100, 64), (2, 17, 129), (4, 1000, 300), (15, 64, 512),
+          (16, 48, 4096), (17, 33, 700), (31, 160, 1024), (32, 5, 2049), (33, 96, 256),
+          (47, 31, 4097), (64, 128, 1000), (65, 127, 384), (100, 300, 2000), (128, 256, 128),
+          (129, 257, 640), (200, 1000, 1111), (255, 130, 3000), (256, 512, 1024),
+          (257, 255, 513), (300, 515, 4224), (513, 520, 896), (1000, 1100, 2500)]
+
+
+@TYPES
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(cuda, M, N, K, dtype):
+    import torch
+    iw, cw, sw = i8_weight(weights(N, K, M))
+    t, cx, sx = i8_tokens(M, K, N)
+    y = Guarded((M, N), tdtype(dtype))
+    assert q.linear_i8_fwd(iw, t, y=y.t) is y.t
+    y.check("y")
+    sums = i8.sums(cx, cw)
+    assert np.array_equal(bits(y.t), round16(scaled(sums, sw, sx), dtype))
+    ref = i8.product(cx, sx, cw, sw)
+    off = np.abs(f64(y.t) - ref)
+    assert np.all(off <= (U16[dtype] + 2.0 ** -21) * np.abs(ref) + 2.0 ** -25)
+    assert torch.equal(q.linear_i8_fwd(iw, t, dtype=tdtype(dtype)), y.t)
+
+
+@pytest.mark.parametrize("M", [1, 3, 20, 64, 100, 300])
+@pytest.mark.parametrize("K", [1 << 12, (1 << 17) - 128])
+def test_largest_sums(cuda, M, K):
+    """Codes at the ends of their range: sums up to 2^31 - 2^21, and with -128
+    (which no quantiser writes) in both up to 2^31 - 2^21 as well."""
+    import torch
+    N = 40
+    for a, b in ((127, 127), (-127, 127), (-128, -128), (-128, 127)):
+        tiles = torch.full((3, K // 64, 4, 16, 16), b, dtype=torch.int8, device="cuda")
+        codes = torch.full((M, K), a, dtype=torch.int8, device="cuda")
+        iw = q.I8Weight(tiles, torch.ones(N, device="cuda"), N, K)
+        t = q.I8Tokens(codes, torch.full((M,), 0.5, device="cuda"), K)
+        want = torch.tensor(float(np.float32(a * b * K)) * 0.5).to(torch.bfloat16)
+        assert (q.linear_i8_fwd(iw, t) == want.cuda()).all()
+
+
+@TYPES
+@pytest.mark.parametrize("M,N,K", [(3, 50, 300), (40, 100, 640), (150, 260, 1000)])
+@pytest.mark.parametrize("left,right", [(0, 3), (1, 0), (4, 4), (16, 16)])
+def test_product_into_strided_rows(cuda, M, N, K, left, right, dtype):
+    import torch
+    iw, cw, sw = i8_weight(weights(N, K, 1))
+    t, cx, sx = i8_tokens(M, K, 2)
+    wide = torch.full((M, left + N + right), 7.0, dtype=tdtype(dtype), device="cuda")
+    y = wide[:, left:left + N]
+    assert q.linear_i8_fwd(iw, t, y=y) is y
+    assert np.array_equal(bits(y), round16(scaled(i8.sums(cx, cw), sw, sx), dtype))
+    assert (wide[:, :left] == 7).all() and (wide[:, left + N:] == 7).all()
+
+
+def test_nan_scales_reach_their_rows_and_columns_only(cuda):
+    import torch
+    for M in (5, 70, 300):
+        N, K = 90, 500
+        w = weights(N, K, 3)
+        w[4, 7] = np.nan
+        x, v = activations(M, K, "bf16", 5)
+        x[2, 1] = float("inf")
+        t, iw = q.quantize_tokens_i8(x), q.quantize_i8(dev(w))
+        y = q.linear_i8_fwd(iw, t)
+        bad = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+        bad[2], bad[:, 4] = True, True
+        assert torch.equal(torch.isnan(y), bad)
+
+
+def test_rows_of_padding_may_hold_anything(cuda):
+    """A weight's rows from N on are never part of a result."""
+    import torch
+    for M in (2, 50, 140):
+        N, K = 21, 256
+        iw, cw, sw = i8_weight(weights(N, K, 8))
+        t, cx, sx = i8_tokens(M, K, 2)
+        tiles = iw.tiles.clone()
+        tiles[1, :, :, 5:] = 99
+        y = q.linear_i8_fwd(q.I8Weight(tiles, iw.scales, N, K), t)
+        assert torch.equal(y, q.linear_i8_fwd(iw, t))
+
+
+def gated_ref(cx, sx, cg, sg, cu, su, act):
+    g, u = i8.product(cx, sx, cg, sg), i8.product(cx, sx, cu, su)
+    a = i8.activation(g, act)
+    z = np.abs(g) if act == "silu" else np.abs(1.5957691216057308 * (g + 0.044715 * g ** 3))
+    return a * u, np.abs(a * u) * 2.0 ** -20 * (3 + z) + 2.0 ** -21 * np.abs(g * u)
+
+
+@TYPES
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 100, 300), (4, 1000, 128), (16, 35, 2000),
+                                   (30, 64, 640), (64, 200, 1000), (65, 130, 512), (128, 128, 256),
+                                   (200, 300, 1500), (300, 513, 1024), (520, 260, 700)])
+def test_gated(cuda, M, N, K, act, dtype):
+    rng = np.random.default_rng(M)
+    gate, cg, sg = i8_weight(weights(N, K, 1) * rng.choice([0.1, 1, 10], (N, 1)).astype(np.float32))
+    up, cu, su = i8_weight(weights(N, K, 2))
+    t, cx, sx = i8_tokens(M, K, 3)
+    y = Guarded((M, N), tdtype(dtype))
+    q.gated_i8_fwd(gate, up, t, act=act, y=y.t)
+    y.check("y")
+    ref, bar = gated_ref(cx, sx, cg, sg, cu, su, act)
+    off = np.abs(f64(y.t) - ref)
+    assert np.all(off <= U16[dtype] * (np.abs(ref) + bar) + bar + 2.0 ** -25)
+    # the two are not exchanged
+    other, _ = gated_ref(cx, sx, cu, su, cg, sg, act)
+    assert M * N * K == 1 or not np.all(np.abs(f64(y.t) - other) <= 0.1 * np.abs(other) + 1e-3)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [6, 80])
+def test_gated_far_ends(cuda, act, M):
+    """Gates from -1e6 to 1e6: the exponential's ends are 0 and g."""
+    import torch
+    N, K = 64, 128
+    cg = np.zeros((N, K), dtype=np.int8)
+    cg[:, 0] = np.linspace(-127, 127, N).round()
+    cu = np.ones((N, K), dtype=np.int8)
+    cx = np.zeros((M, K), dtype=np.int8)
+    cx[:, 0] = 1
+    one = np.ones(N, dtype=np.float32)
+    sx = np.geomspace(1e-3, 1e4, M).astype(np.float32)
+    t = q.I8Tokens(dev(cx), dev(sx), K)
+    gate = q.I8Weight(dev(i8.tile(cg)), dev(one), N, K)
+    up = q.I8Weight(dev(i8.tile(cu)), dev(one), N, K)
+    y = q.gated_i8_fwd(gate, up, t, act=act)
+    ref, bar = gated_ref(cx, sx, cg, one, cu, one, act)
+    with np.errstate(over="ignore"):
+        g = i8.product(cx, sx, cg, one)
+    floor = np.abs(g * i8.product(cx, sx, cu, one)) * 2.0 ** -120
+    assert torch.isfinite(y).all()
+    assert np.all(np.abs(f64(y) - ref) <= U16["bf16"] * (np.abs(ref) + bar) + bar + floor)
+
+
+# ---------------------------------------------------------------------------
+# as they are used
+# ---------------------------------------------------------------------------
+
+def test_empty_calls(cuda):
+    import torch
+    iw, _, _ = i8_weight(weights(5, 70, 1))
+    x = torch.zeros(0, 70, dtype=torch.bfloat16, device="cuda")
+    t = q.quantize_tokens_i8(x)
+    assert t.M == 0 and q.dequantize_tokens_i8(t).shape == (0, 70)
+    assert q.linear_i8_fwd(iw, t).shape == (0, 5) and q.gated_i8_fwd(iw, iw, t).shape == (0, 5)
+    w = torch.ones(70, dtype=torch.bfloat16, device="cuda")
+    t, h = q.rms_norm_i8(x, w, 1e-5, residual=x)
+    assert t.M == 0 and h.shape == (0, 70)
+
+
+def test_python_refusals_on_the_gpu(cuda):
+    import torch
+    iw, _, _ = i8_weight(weights(20, 256, 1))
+    t, _, _ = i8_tokens(3, 256, 1)
+    t2, _, _ = i8_tokens(3, 255, 1)
+    x = torch.zeros(3, 256, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(3, 20, dtype=torch.bfloat16, device="cuda")
+    for f in (lambda: q.linear_i8_fwd(iw, t2),
+              lambda: q.linear_i8_fwd(iw, t, y=y[:2]),
+              lambda: q.linear_i8_fwd(iw, t, y=y.float()),
+              lambda: q.linear_i8_fwd(iw, t, y=y, dtype=torch.float16),
+              lambda: q.linear_i8_fwd(iw, t, dtype=torch.float32),
+              lambda: q.linear_i8_fwd(iw, t, y=torch.zeros(20, 3, dtype=torch.bfloat16, device="cuda").t()),
+              lambda: q.gated_i8_fwd(iw, iw, t, act="relu"),
+              lambda: q.gated_i8_fwd(iw, i8_weight(weights(21, 256, 1))[0], t),
+              lambda: q.I8Weight(iw.tiles, iw.scales, 20, 250 + 128),
+              lambda: q.I8Weight(iw.tiles, iw.scales[:19], 20, 256),
+              lambda: q.I8Tokens(t.codes, t.scales, 257),
+              lambda: q.I8Tokens(t.codes[:, :128], t.scales, 128),
+              lambda: q.quantize_tokens_i8(x.float()),
+              lambda: q.quantize_tokens_i8(x, out=t2),
+              lambda: q.rms_norm_i8(x, w[:255], 1e-5),
+              lambda: q.rms_norm_i8(x, w.half(), 1e-5),
+              lambda: q.rms_norm_i8(x, w, 1e-5, residual=x[:2]),
+              lambda: q.rms_norm_i8(x, w, 1e-5, h=x),
+              lambda: q.rms_norm_i8(x.t(), w[:3], 1e-5)):
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(q.QloraError, match="EINVAL"):
+        q.rms_norm_i8(x, w, -1.0)
+    with pytest.raises(q.QloraError, match="EINVAL"):
+        q.rms_norm_i8(x, w, 1e-5, residual=x.clone(), h=w.expand(3, 256))
+
+
+def test_handles_follow_their_tensors(cuda):
+    import torch
+    iw, cw, sw = i8_weight(weights(33, 300, 1))
+    t, cx, sx = i8_tokens(4, 300, 2)
+    y = q.linear_i8_fwd(iw, t)
+    iw.scales, t.scales = iw.scales * 2, t.scales * 2
+    assert torch.equal(q.linear_i8_fwd(iw, t), y * 4)
+    t.scales = t.scales[:3]
+    with pytest.raises(ValueError):
+        q.linear_i8_fwd(iw, t)
+
+
+def test_merge_to_8_bits(cuda):
+    import torch
+    w = dev(weights(128, 256, 3))
+    A = (torch.randn(8, 256, device="cuda") * 0.1).to(torch.bfloat16)
+    B = (torch.randn(128, 8, device="cuda") * 0.1).to(torch.bfloat16)
+    f, _, iw = q.merge_adapter(w, A, B, 16.0, requantize="i8")
+    c, s = i8.encode(f.cpu().numpy())
+    assert np.array_equal(iw.tiles.cpu().numpy(), i8.tile(c))
+    assert np.array_equal(iw.scales.cpu().numpy(), s)
+
+
+def test_another_stream(cuda):
+    import torch
+    x, v = activations(130, 700, "bf16", 1)
+    iw, cw, sw = i8_weight(weights(260, 700, 2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y = q.linear_i8_fwd(iw, q.quantize_tokens_i8(x))
+    torch.cuda.current_stream().wait_stream(side)
+    c, s = i8.encode(v)
+    assert np.array_equal(bits(y), round16(scaled(i8.sums(c, cw), sw, s), "bf16"))
+
+
+class Block:
+    """The 8-bit half of a served layer: norm, gated MLP, norm, projection."""
+
+    def __init__(self, hidden, ffn, dtype):
+        import torch
+        self.w1, self.w2 = ((1 + 0.1 * torch.randn(hidden, device="cuda")).to(tdtype(dtype))
+                            for _ in range(2))
+        self.gate, self.up = (q.quantize_i8(torch.randn(ffn, hidden, device="cuda") * 0.02)
+                              for _ in range(2))
+        self.down = q.quantize_i8(torch.randn(hidden, ffn, device="cuda") * 0.02)
+        self.out = q.quantize_i8(torch.randn(hidden + 100, hidden, device="cuda") * 0.02)
+        self.dt = tdtype(dtype)
+
+    def __call__(self, x, stream):
+        t, h = q.rms_norm_i8(x, self.w1, 1e-5, residual=stream, h=stream)
+        a = q.gated_i8_fwd(self.gate, self.up, t, dtype=self.dt)
+        d = q.linear_i8_fwd(self.down, q.quantize_tokens_i8(a), dtype=self.dt)
+        t, h = q.rms_norm_i8(d, self.w2, 1e-5, residual=h, h=h)
+        return q.linear_i8_fwd(self.out, t, dtype=self.dt), h
+
+    def plain(self, x, stream):
+        """The same in fp64 from the weights' values, roundings to 16 bits
+        and to 8 as the calls have them."""
+        import torch
+
+        def tokens(v):
+            a = v.abs().amax(-1, keepdim=True)
+            return torch.round(127 * v / a) * (a / 127)
+
+        def norm(h, w):
+            return tokens(h.double() * w.double() * (h.double().square().mean(-1, keepdim=True) + 1e-5).rsqrt())
+
+        def values(w):
+            n, k = w.N, w.K
+            c = w.tiles.permute(0, 3, 1, 2, 4).reshape(w.tiles.shape[0] * 16, -1)[:n, :k]
+            return c.double() * w.scales.double()[:, None]
+
+        h = (x.float() + stream.float()).to(self.dt)
+        t = norm(h, self.w1)
+        g, u = t @ values(self.gate).T, t @ values(self.up).T
+        a = (torch.nn.functional.silu(g) * u).to(self.dt)
+        d = (tokens(a.double()) @ values(self.down).T).to(self.dt)
+        h = (d.float() + h.float()).to(self.dt)
+        return norm(h, self.w2) @ values(self.out).T, h
+
+
+@TYPES
+@pytest.mark.parametrize("M", [1, 7, 200])
+def test_a_block_runs_together(cuda, M, dtype):
+    """Every product's output has a rounding of u to 16 bits; where that lands
+    a value on another code, or its row's scale on another, one step of 8 bits
+    (a / 127) follows.  In the norm over the whole output: the gated values
+    are off by u each, d by at most (u + the steps of the codes that change)
+    of itself.  A value changes its code with probability u |v| 127 / a, then
+    by a step: its square's mean is u |v| a / 127 <= u a^2 / 127, against a
+    row's mean square of a^2 / 12 or more here (a is below 3.5 times the
+    root-mean-square of 100 values and more: normal tails aside, 6 times).
+    So the relative norm is at most sqrt(36 u / 127) + 2 u for each of the two
+    codings that follow a rounding, and they add."""
+    import torch
+    torch.manual_seed(M)
+    b = Block(512, 1100, dtype)
+    x = torch.randn(M, 512, device="cuda").to(b.dt)
+    stream = (2 * torch.randn(M, 512, device="cuda")).to(b.dt)
+    want, wh = b.plain(x, stream)
+    y, h = b(x, stream)
+    u = U16[dtype]
+    bar = 2 * ((36 * u / 127) ** 0.5 + 2 * u)
+    assert float((y.double() - want).norm() / want.norm()) <= bar
+    assert float((h.double() - wh.double()).norm() / wh.double().norm()) <= bar
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_captured_and_replayed(cuda, M):
+    """A captured block, replayed with other inputs in the same places, gives
+    the eager call's bits; eager work runs between the replays."""
+    import torch
+    torch.manual_seed(1)
+    b = Block(384, 900, "bf16")
+    x, s = (torch.zeros(M, 384, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b(x, s)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = b(x, s)
+    for i in range(4):
+        nx, ns = (torch.randn(M, 384, device="cuda").to(torch.bfloat16) for _ in range(2))
+        want, wh = b(nx, ns.clone())
+        x.copy_(nx)
+        s.copy_(ns)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(h, wh)
+
+
+def test_same_bits_on_every_run(cuda):
+    import torch
+    iw, _, _ = i8_weight(weights(500, 1100, 2))
+    for M in (3, 90, 700):
+        t, _, _ = i8_tokens(M, 1100, M)
+        first = q.linear_i8_fwd(iw, t)
+        for _ in range(3):
+            assert torch.equal(q.linear_i8_fwd(iw, t), first)
+        # and for a token alone
+        one = q.I8Tokens(t.codes[M - 1:], t.scales[M - 1:], 1100)
+        assert torch.equal(q.linear_i8_fwd(iw, one), first[M - 1:])
