@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["api.cpp", "nf4_table.cpp", "quant_kernels.hip", "lora_kernels.hip",
            "gemm_fwd.hip", "gemm_bwd.hip", "gemm_decode.hip", "merge.hip", "noalloc.hip",
            "api_u4.cpp", "u4_quant.hip", "u4_linear.hip", "kv4_cache.hip",
-           "kv4_attention.hip", "api_i8.cpp", "i8_rows.hip", "i8_weight.hip", "i8_linear.hip"]
+           "kv4_attention.hip", "api_i8.cpp", "i8_rows.hip", "i8_weight.hip", "i8_linear.hip",
+           "i8_gemm.hip"]
 
 ARCH = "gfx950"
 HIP_FLAGS = [

@@ -237,6 +237,16 @@ __device__ __forceinline__ uint32_t buffer_load1(__amdgpu_buffer_rsrc_t r, uint3
   return __builtin_amdgcn_raw_buffer_load_b8(r, (int)voff, (int)soff, 0);
 }
 
+// Stands between LDS writes of a wave's lanes and reads of the same place by
+// its other lanes.  The hardware does one wave's LDS operations in order, so
+// it is no instruction; it keeps the compiler, which sees one lane, from
+// moving them past each other.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Block-to-tile mapping for a 1-D grid of `total` blocks.  Consecutive
 // workgroup ids are dealt round-robin to the 8 XCDs (each with its own L2),
 // so id i is first turned into a rank that is contiguous within its XCD;

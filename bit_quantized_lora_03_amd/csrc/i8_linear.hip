@@ -14,6 +14,8 @@
 namespace qlora {
 namespace {
 
+constexpr int64_t kFewTokens = 64;
+
 __device__ __forceinline__ i32x4_t mfma16(u32x4_t a, u32x4_t b, i32x4_t c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a),
                                                __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
@@ -145,9 +147,13 @@ void pick(const I8LinearArg& p, hipStream_t s) {
 
 }  // namespace
 
-size_t linear_i8_workspace(int64_t, int64_t, int64_t, bool) { return 0; }
+size_t linear_i8_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
+  return M <= kFewTokens ? 0 : gemm_i8_workspace(gemm_i8_plan(M, N, K, gated), gated);
+}
 
-hipError_t launch_linear_i8(const I8LinearArg& p, int32_t*, bool f16, hipStream_t s) {
+hipError_t launch_linear_i8(const I8LinearArg& p, int32_t* workspace, bool f16, hipStream_t s) {
+  if (p.M > kFewTokens)
+    return launch_gemm_i8(p, gemm_i8_plan(p.M, p.N, p.K, p.tiles[1] != nullptr), workspace, f16, s);
   if (p.tiles[1]) {
     if (f16)
       pick<F16T, 2>(p, s);

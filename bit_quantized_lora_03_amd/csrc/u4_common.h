@@ -142,16 +142,6 @@ __device__ __forceinline__ void u4_values8(uint32_t w, uint32_t pair, float (&v)
   for (int i = 0; i < 8; ++i) v[i] = fmaf(s, (float)((w >> (4 * i)) & 15u), m);
 }
 
-// Stands between LDS writes of a wave's lanes and reads of the same place by
-// its other lanes.  The hardware does one wave's LDS operations in order, so
-// it is no instruction; it keeps the compiler, which sees one lane, from
-// moving them past each other.
-__device__ __forceinline__ void wave_exchange() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // ---- reductions over 8, 16 or 32 neighbouring lanes ------------------------
 // Each step brings every lane the value of a lane that holds the other half
 // of the lanes combined so far.
