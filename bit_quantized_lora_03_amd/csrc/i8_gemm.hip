@@ -90,75 +90,87 @@ struct GemmArg {
   i32x4_t* part;  // [tail_s][tail_q][wave][JT][NI][4][64]
 };
 
-// A wave's outputs of 32 tokens: RO rows from n0 on of the tokens from m0 on.
-// Through the wave's LDS, so that stores are runs of a token's row.
-template <class DT, int NI, int G>
-struct Slice {
+// A wave's outputs: RO rows from n0 on of the 32 J tokens from m0 on.  All of
+// them are scaled into the wave's LDS first, and go out from there in a loop,
+// in runs of a token's row: done for 32 tokens at a time, with a wait between
+// each write and read and code for every one, it took 10 us a tile of 256 x
+// 256, a tenth of the time at K 8192.
+template <class DT, int NI, int G, int J>
+struct Outputs {
   static constexpr int RO = G == 2 ? 32 : 32 * NI;
-  static constexpr int LD = RO * 2 + 16;  // bytes of a token in LDS
-  static constexpr int kBytes = 32 * LD;
-  f32x4_t sw[NI][4];  // the lane's rows
-  __amdgpu_buffer_rsrc_t xs;
+  static constexpr int PR = RO / 8;              // 16-byte pieces of a token
+  static constexpr int kBytes = 32 * J * RO * 2;  // of LDS
+  // where piece c of a token is: 16 neighbouring tokens' in different banks
+  static __device__ int place(int tok, int c) {
+    return tok * PR + (c ^ (PR == 8 ? (tok >> 1) & 7 : (tok >> 2) & 3));
+  }
 
-  __device__ void scales(const I8LinearArg& p, int64_t n0, int lane) {
-    xs = make_rsrc(p.xscale, (uint32_t)(p.M * 4));
+  template <class Acc>
+  static __device__ void run(const Acc& acc, const I8LinearArg& p, int64_t n0, int64_t m0,
+                             uint8_t* lds, int lane) {
+    const int lr = lane & 31, lg = lane >> 5;
+    f32x4_t sw[NI][4];  // the lane's rows; past N and M: zero
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const auto ws = make_rsrc(p.wscale[G == 2 ? i : 0], (uint32_t)(p.N * 4));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + (G == 2 ? 0 : 32 * i) + 8 * q + 4 * (lane >> 5);
-        // past N: zero
-        sw[i][q] = __builtin_bit_cast(f32x4_t, buffer_load16(ws, (uint32_t)(n * 4)));
-      }
+      for (int q = 0; q < 4; ++q)
+        sw[i][q] = __builtin_bit_cast(
+            f32x4_t, buffer_load16(ws, (uint32_t)(n0 + (G == 2 ? 0 : 32 * i) + 8 * q + 4 * lg) * 4));
     }
-  }
-  __device__ void store(const i32x16_t (&acc)[NI], const I8LinearArg& p, int64_t n0, int64_t m0,
-                        uint8_t* lds, int lane) {
-    const int lr = lane & 31, lg = lane >> 5;
-    const float sx = __uint_as_float(
-        __builtin_amdgcn_raw_buffer_load_b32(xs, (int)((m0 + lr) * 4), 0, 0));
+    float sx[J];
+    const auto xs = make_rsrc(p.xscale, (uint32_t)(p.M * 4));
 #pragma unroll
-    for (int i = 0; i < (G == 2 ? 1 : NI); ++i)
+    for (int j = 0; j < J; ++j)
+      sx[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          xs, (int)((uint32_t)(m0 + 32 * j + lr) * 4), 0, 0));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[4];
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = i8_scaled(acc[i][4 * q + j], sw[i][q][j], sx);
-          if constexpr (G == 2)
-            v[j] = gated(v[j], i8_scaled(acc[1][4 * q + j], sw[1][q][j], sx), p.act);
+      for (int i = 0; i < (G == 2 ? 1 : NI); ++i) {
+        // (as wholes up to here, or the compiler copies all sums out of the
+        // accumulators' registers before the first is used, and spills)
+        i32x16_t a = acc[j][i], b = acc[j][G - 1];
+        asm volatile("" : "+a"(a));
+        if constexpr (G == 2) asm volatile("" : "+a"(b));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = i8_scaled(a[4 * q + e], sw[i][q][e], sx[j]);
+            if constexpr (G == 2) v[e] = gated(v[e], i8_scaled(b[4 * q + e], sw[1][q][e], sx[j]), p.act);
+          }
+          *reinterpret_cast<u32x2_t*>(lds + 16 * place(32 * j + lr, 4 * i + q) + 8 * lg) =
+              u32x2_t{DT::pack2(v[0], v[1]), DT::pack2(v[2], v[3])};
         }
-        *reinterpret_cast<u32x2_t*>(lds + lr * LD + (32 * i + 8 * q + 4 * lg) * 2) =
-            u32x2_t{DT::pack2(v[0], v[1]), DT::pack2(v[2], v[3])};
+        __builtin_amdgcn_sched_barrier(0);
       }
     wave_exchange();
-    constexpr int PR = RO / 8;  // 16-byte pieces of a token
-    const bool whole = ((uintptr_t)p.y & 15) == 0 && p.ldy % 8 == 0;
-#pragma unroll
-    for (int t = 0; t < 32 * PR / 64; ++t) {
-      const int tok = (64 * t + lane) / PR, c = lane % PR;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(lds + tok * LD + 16 * c);
-      const int64_t m = m0 + tok, n = n0 + 8 * c;
-      if (m < p.M && n < p.N) {
-        uint16_t* y = p.y + m * p.ldy + n;
-        if (whole && n + 8 <= p.N) {
-          *reinterpret_cast<u32x4_t*>(y) = v;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (n + j < p.N) y[j] = (uint16_t)half_of(v, j);
-        }
+    const int c = lane % PR, t0 = lane / PR;
+    uint16_t* y = p.y + (m0 + t0) * p.ldy + n0 + 8 * c;
+    const int64_t step = 64 / PR * p.ldy;
+    if (((uintptr_t)p.y & 15) == 0 && p.ldy % 8 == 0 && m0 + 32 * J <= p.M && n0 + RO <= p.N) {
+#pragma unroll 4
+      for (int t = 0; t < J * PR / 2; ++t, y += step)
+        *reinterpret_cast<u32x4_t*>(y) =
+            *reinterpret_cast<const u32x4_t*>(lds + 16 * place(t0 + 64 / PR * t, c));
+    } else {
+#pragma nounroll
+      for (int t = 0; t < J * PR / 2; ++t, y += step) {
+        const u32x4_t v =
+            *reinterpret_cast<const u32x4_t*>(lds + 16 * place(t0 + 64 / PR * t, c));
+        if (m0 + t0 + 64 / PR * t < p.M)
+          store_piece(y, 0, (int)min(p.N - n0 - 8 * c, (int64_t)8), v);
       }
     }
-    wave_exchange();
   }
 };
 
 template <class DT, int NI, int JT, int G>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, JT == 8 ? 1 : 2)))
 void gemm_i8_kernel(GemmArg g) {
-  using S = Slice<DT, NI, G>;
+  using S = Outputs<DT, NI, G, JT>;
   constexpr int TM = 32 * JT, RO = S::RO, TN = 4 * RO;
   constexpr int XR = JT;               // DMA instructions of a wave a tile
   constexpr int LC = 4 * NI;           // loads of weights a tile
@@ -173,8 +185,9 @@ void gemm_i8_kernel(GemmArg g) {
   const uint32_t m_tiles = (uint32_t)((p.M + TM - 1) / TM), n_tiles = (uint32_t)((p.N + TN - 1) / TN);
   const Part w = part_of(blockIdx.x, m_tiles, n_tiles, g.plan);
   const int64_t m0 = (int64_t)w.m * TM, n0 = (int64_t)w.n * TN;
-  const int nkt = (int)(Kp / KT);
-  const int kt0 = (int)((uint32_t)(nkt * w.z) / w.nz), kt1 = (int)((uint32_t)(nkt * (w.z + 1)) / w.nz);
+  const int nkt = (int)(Kp / KT), pairs = (nkt + 1) / 2;
+  const int kt0 = 2 * (int)((uint32_t)(pairs * w.z) / w.nz),
+            kt1 = min(nkt, 2 * (int)((uint32_t)(pairs * (w.z + 1)) / w.nz));
 
   // Operands of a weight: lane l has row l % 32 and 16 columns of a step of
   // 32.  Panels past the end read as zeros (the range check covers the lane's
@@ -182,14 +195,17 @@ void gemm_i8_kernel(GemmArg g) {
   const uint32_t panel = 16 * (uint32_t)Kp;
   const int64_t left = n_panels - n0 / 16;
   const uint32_t held = (uint32_t)min(left, (int64_t)(TN / 16)) * panel;
-  const auto wbuf0 = make_rsrc(p.tiles[0] + (n0 / 16) * panel, held);
-  const auto wbuf1 = make_rsrc(p.tiles[G - 1] + (n0 / 16) * panel, held);
+  const int8_t* const w0 = p.tiles[0] + (n0 / 16) * panel;
+  const int8_t* const w1 = p.tiles[G - 1] + (n0 / 16) * panel;
   uint32_t wo[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
     wo[i] = (wave * (RO / 16) + (G == 2 ? 0 : 2 * i) + (lr >> 4)) * panel + lg * 256 + (lr & 15) * 16;
+  // Tiles are worked on in pairs; weights of one past the last are zeros (a
+  // buffer of no bytes).
   auto load_w = [&](int kt, int i, int kk) -> u32x4_t {
-    return buffer_load16(G == 2 && i == 1 ? wbuf1 : wbuf0, wo[i] + (kk >> 1) * 1024 + (kk & 1) * 512,
+    const auto buf = make_rsrc(G == 2 && i == 1 ? w1 : w0, kt < kt1 ? held : 0);
+    return buffer_load16(buf, wo[i] + (kk >> 1) * 1024 + (kk & 1) * 512,
                          (uint32_t)kt * (2 * kI8Tile));
   };
   // Tokens: DMA q of the wave fills the 1 KiB from row 8 (XR wave + q) on,
@@ -241,7 +257,7 @@ void gemm_i8_kernel(GemmArg g) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) W[1][kk][i] = load_w(cl(kt0 + 1), i, kk);
+      for (int i = 0; i < NI; ++i) W[1][kk][i] = load_w(kt0 + 1, i, kk);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(wait_imm(XR + 2 * LC));
     __builtin_amdgcn_s_barrier();
@@ -265,25 +281,26 @@ void gemm_i8_kernel(GemmArg g) {
             X[(kk + 1) & 1][j] = kk < 3 ? read_x(now, kk + 1, j) : read_x(next, 0, j);
           const int slot = SLOTS * kk + s;
           if (slot % DP == DP - 1) dma_x(fill, cl(kt + 3), slot / DP);
+          // the registers of the step before are free
+          if (kk > 0 && s % (SLOTS / NI) == SLOTS / NI / 2 - 1)
+            W[ph][kk - 1][s / (SLOTS / NI)] = load_w(kt + 2, s / (SLOTS / NI), kk - 1);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int i = 0; i < NI; ++i) W[ph][kk][i] = load_w(cl(kt + 2), i, kk);
+      for (int i = 0; i < NI; ++i) W[ph][3][i] = load_w(kt + 2, i, 3);
       __builtin_amdgcn_sched_barrier(0);
-      // x of tile kt + 2, which the last iteration asked for before its weights
-      __builtin_amdgcn_s_waitcnt(wait_imm(XR + 2 * LC));
+      // x of tile kt + 2: all that the last iteration asked for but its last
+      // weights
+      __builtin_amdgcn_s_waitcnt(wait_imm(XR + LC + NI));
       __builtin_amdgcn_s_barrier();
     };
     int stage = 0, kt = kt0;
     auto at = [&](int d) { return lds + ((stage + d) & (kStages - 1)) * XST; };
-    for (; kt + 2 <= kt1; kt += 2, stage += 2) {
+    for (; kt < kt1; kt += 2, stage += 2) {
       iteration(kt, std::integral_constant<int, 0>(), at(0), at(1), at(3));
       iteration(kt + 1, std::integral_constant<int, 1>(), at(1), at(2), at(4));
     }
-    if (kt < kt1) iteration(kt, std::integral_constant<int, 0>(), at(0), at(1), at(3));
     // what was asked for past the end is still on its way to LDS
     __builtin_amdgcn_s_waitcnt(wait_imm(0));
   }
@@ -294,24 +311,23 @@ void gemm_i8_kernel(GemmArg g) {
 #pragma unroll
     for (int j = 0; j < JT; ++j)
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+      for (int i = 0; i < NI; ++i) {
+        i32x16_t a = acc[j][i];
+        asm volatile("" : "+a"(a));
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          o[((j * NI + i) * 4 + q) * 64] = i32x4_t{acc[j][i][4 * q], acc[j][i][4 * q + 1],
-                                                   acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+          o[((j * NI + i) * 4 + q) * 64] =
+              i32x4_t{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+      }
   } else {
-    S out;
-    out.scales(p, n0 + wave * RO, lane);
-    uint8_t* scratch = lds + wave * S::kBytes;
-#pragma unroll
-    for (int j = 0; j < JT; ++j) out.store(acc[j], p, n0 + wave * RO, m0 + 32 * j, scratch, lane);
+    S::run(acc, p, n0 + wave * RO, m0, lds + wave * S::kBytes, lane);
   }
 }
 
 // The tail's sums over its splits: a wave has 32 tokens of a wave's tile.
 template <class DT, int NI, int JT, int G>
 __global__ __launch_bounds__(256) void join_i8_kernel(GemmArg g) {
-  using S = Slice<DT, NI, G>;
+  using S = Outputs<DT, NI, G, 1>;
   constexpr int TM = 32 * JT, RO = S::RO, TN = 4 * RO;
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * S::kBytes];
   const I8LinearArg& p = g.a;
@@ -323,15 +339,13 @@ __global__ __launch_bounds__(256) void join_i8_kernel(GemmArg g) {
           (uint32_t)((p.N + TN - 1) / TN), m, n);
   const int64_t n0 = (int64_t)n * TN + owner * RO, m0 = (int64_t)m * TM + 32 * j;
   if (n0 >= p.N || m0 >= p.M) return;
-  S out;
-  out.scales(p, n0, lane);
   const int64_t stride = (int64_t)g.plan.tail_q * 4 * JT * NI * 4 * 64;
   const i32x4_t* src = g.part + (int64_t)piece * (NI * 4 * 64) + lane;
-  i32x16_t acc[NI];
+  i32x16_t acc[1][NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[i][v] = 0;
+    for (int v = 0; v < 16; ++v) acc[0][i][v] = 0;
   for (int z = 0; z < g.plan.tail_s; ++z, src += stride)
 #pragma unroll
     for (int i = 0; i < NI; ++i)
@@ -339,9 +353,9 @@ __global__ __launch_bounds__(256) void join_i8_kernel(GemmArg g) {
       for (int q = 0; q < 4; ++q) {
         const i32x4_t v = src[(i * 4 + q) * 64];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][4 * q + e] += v[e];
+        for (int e = 0; e < 4; ++e) acc[0][i][4 * q + e] += v[e];
       }
-  out.store(acc, p, n0, m0, lds + wave * S::kBytes, lane);
+  S::run(acc, p, n0, m0, lds + wave * S::kBytes, lane);
 }
 
 template <class DT, int NI, int JT, int G>
@@ -354,10 +368,16 @@ void go(const GemmArg& g, hipStream_t s) {
 
 template <class DT, int G>
 void pick(const GemmArg& g, hipStream_t s) {
-  if (g.plan.tm == 256)
-    go<DT, 2, 8, G>(g, s);
-  else
-    go<DT, 2, 4, G>(g, s);
+  const I8GemmPlan& p = g.plan;
+  if (G == 2 || p.tn == 256) {
+    if (p.tm == 256) return go<DT, 2, 8, G>(g, s);
+    if (p.tm == 128) return go<DT, 2, 4, G>(g, s);
+    return go<DT, 2, 2, G>(g, s);
+  }
+  if constexpr (G == 1) {
+    if (p.tm == 128) return go<DT, 1, 4, G>(g, s);
+    return go<DT, 1, 2, G>(g, s);
+  }
 }
 
 }  // namespace
