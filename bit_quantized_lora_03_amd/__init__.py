@@ -48,8 +48,7 @@ from ._lib import (  # noqa: F401
 _U4 = ("Kv4Cache", "U4Weight", "dequantize_u4", "kv4_append", "kv4_attention",
        "kv4_attention_workspace_bytes", "kv4_read", "linear_u4_fwd", "quantize_u4")
 _I8 = ("I8Tokens", "I8Weight", "dequantize_i8", "dequantize_tokens_i8", "gated_i8_fwd",
-       "linear_i8_fwd", "linear_i8_workspace_bytes", "quantize_i8", "quantize_tokens_i8",
-       "rms_norm_i8")
+       "linear_i8_fwd", "quantize_i8", "quantize_tokens_i8", "rms_norm_i8")
 
 
 def __getattr__(name):

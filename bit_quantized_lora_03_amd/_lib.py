@@ -41,7 +41,7 @@ EXPORTS = ("qlora_quantize_nf4", "qlora_double_quant", "qlora_quantize_nf4_dq",
            "qlora_quantize_i8", "qlora_dequantize_i8", "qlora_dequantize_i8_f16",
            "qlora_quantize_tokens_i8", "qlora_quantize_tokens_i8_f16",
            "qlora_dequantize_tokens_i8", "qlora_dequantize_tokens_i8_f16",
-           "qlora_rms_norm_i8", "qlora_rms_norm_i8_f16", "qlora_linear_i8_workspace_bytes",
+           "qlora_rms_norm_i8", "qlora_rms_norm_i8_f16",
            "qlora_linear_i8_fwd", "qlora_linear_i8_fwd_f16",
            "qlora_gated_i8_fwd", "qlora_gated_i8_fwd_f16")
 
@@ -117,8 +117,8 @@ def lib() -> ctypes.CDLL:
                    ctypes.c_double)
     tokens = [vp, i64, i64, i64, vp, vp, vp]
     norm = [vp, i64, vp, i64, vp, f64, i64, i64, vp, i64, vp, vp, vp]
-    product = [iw, it, vp, i64, vp, sz, vp]
-    gated = [iw, iw, i32, it, vp, i64, vp, sz, vp]
+    product = [iw, it, vp, i64, vp]
+    gated = [iw, iw, i32, it, vp, i64, vp]
     attend = [cp, bp, vp, i64, i64, i32, f32, i32, i32, i64, vp, vp, vp, sz, vp]
     sig = {
         "qlora_quantize_nf4": ([vp, i64, i32, vp, vp, vp], ctypes.c_int),
@@ -176,7 +176,6 @@ def lib() -> ctypes.CDLL:
         "qlora_dequantize_tokens_i8_f16": ([it, vp, vp], ctypes.c_int),
         "qlora_rms_norm_i8": (norm, ctypes.c_int),
         "qlora_rms_norm_i8_f16": (norm, ctypes.c_int),
-        "qlora_linear_i8_workspace_bytes": ([i64, i64, i64, i32], sz),
         "qlora_linear_i8_fwd": (product, ctypes.c_int),
         "qlora_linear_i8_fwd_f16": (product, ctypes.c_int),
         "qlora_gated_i8_fwd": (gated, ctypes.c_int),

@@ -163,8 +163,7 @@ int norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
 }
 
 int linear(const qlora_i8_weight* w, const qlora_i8_weight* up, bool gated, int32_t act,
-           const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* workspace, size_t ws_bytes,
-           void* stream, bool f16) {
+           const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* stream, bool f16) {
   try {
     int st = check_weight(w);
     if (st != QLORA_OK) return st;
@@ -181,13 +180,8 @@ int linear(const qlora_i8_weight* w, const qlora_i8_weight* up, bool gated, int3
         ((x->M + 63) / 64) * ((w->N + 63) / 64) >= (int64_t{1} << 22))
       return QLORA_ESHAPE;
     if (!aligned(y, 2)) return QLORA_EALIGN;
-    const size_t need = qlora::linear_i8_workspace(x->M, w->N, w->K, gated);
-    if (need > 0) {
-      if (!workspace || ws_bytes < need) return QLORA_EWORKSPACE;
-      if (!aligned(workspace, 256)) return QLORA_EALIGN;
-    }
     const size_t tb = tile_bytes(w->N, w->K), sb = (size_t)w->N * 4;
-    if (clash<2, 6>({{y, rows_bytes(x->M, ldy, w->N)}, {need > 0 ? workspace : nullptr, need}},
+    if (clash<1, 6>({{y, rows_bytes(x->M, ldy, w->N)}},
                     {{w->tiles, tb},
                      {w->scales, sb},
                      {gated ? up->tiles : nullptr, tb},
@@ -205,8 +199,7 @@ int linear(const qlora_i8_weight* w, const qlora_i8_weight* up, bool gated, int3
                                w->N,
                                w->K,
                                act};
-    return hip_status(qlora::launch_linear_i8(p, need > 0 ? static_cast<int32_t*>(workspace) : nullptr,
-                                              f16, as_stream(stream)));
+    return hip_status(qlora::launch_linear_i8(p, f16, as_stream(stream)));
   } catch (...) {
     return QLORA_EHIP;
   }
@@ -266,33 +259,22 @@ int qlora_rms_norm_i8_f16(const uint16_t* x, int64_t ldx, const uint16_t* residu
   return norm(x, ldx, residual, ldr, weight, eps, M, K, h, ldh, codes, scales, stream, true);
 }
 
-size_t qlora_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t gated) {
-  try {
-    if (M <= 0 || M > kMaxLinearM || check_size(N, K) != QLORA_OK) return 0;
-    return qlora::linear_i8_workspace(M, N, K, gated != 0);
-  } catch (...) {
-    return 0;
-  }
-}
-
 int qlora_linear_i8_fwd(const qlora_i8_weight* w, const qlora_i8_tokens* x, uint16_t* y,
-                        int64_t ldy, void* workspace, size_t ws_bytes, void* stream) {
-  return linear(w, nullptr, false, 0, x, y, ldy, workspace, ws_bytes, stream, false);
+                        int64_t ldy, void* stream) {
+  return linear(w, nullptr, false, 0, x, y, ldy, stream, false);
 }
 int qlora_linear_i8_fwd_f16(const qlora_i8_weight* w, const qlora_i8_tokens* x, uint16_t* y,
-                            int64_t ldy, void* workspace, size_t ws_bytes, void* stream) {
-  return linear(w, nullptr, false, 0, x, y, ldy, workspace, ws_bytes, stream, true);
+                            int64_t ldy, void* stream) {
+  return linear(w, nullptr, false, 0, x, y, ldy, stream, true);
 }
 
 int qlora_gated_i8_fwd(const qlora_i8_weight* gate, const qlora_i8_weight* up, int32_t act,
-                       const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* workspace,
-                       size_t ws_bytes, void* stream) {
-  return linear(gate, up, true, act, x, y, ldy, workspace, ws_bytes, stream, false);
+                       const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* stream) {
+  return linear(gate, up, true, act, x, y, ldy, stream, false);
 }
 int qlora_gated_i8_fwd_f16(const qlora_i8_weight* gate, const qlora_i8_weight* up, int32_t act,
-                           const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* workspace,
-                           size_t ws_bytes, void* stream) {
-  return linear(gate, up, true, act, x, y, ldy, workspace, ws_bytes, stream, true);
+                           const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* stream) {
+  return linear(gate, up, true, act, x, y, ldy, stream, true);
 }
 
 }  // extern "C"

@@ -1,12 +1,11 @@
 // Products of 8-bit tokens with 8-bit weights for many tokens (i8_linear.hip
 // has the formula and the form for few).
 //
-// Bound by the matrix cores.  A block of four waves has a tile of 128 NI
-// weight rows and 32 JT tokens; wave w has 32 NI of the rows against all the
-// tokens, NI x JT accumulators of the 32 x 32 x 32 instruction.  With two
-// weights (G = 2) accumulator 0 is of the gate's rows and 1 of the same rows of
-// the other, so a lane has both sums of an output.  K goes by in tiles of 128
-// columns.
+// A block of four waves has a tile of 128 NI weight rows and 32 JT tokens; wave
+// w has 32 NI of the rows against all the tokens, NI x JT accumulators of the
+// 32 x 32 x 32 instruction.  With two weights (G = 2) accumulator 0 is of the
+// gate's rows and 1 of the same rows of the other, so a lane has both sums of an
+// output.  K goes by in tiles of 128 columns.
 //
 // Weights come from memory into registers as operands (their tiles are in that
 // order, so a load is runs of 512 bytes) and never pass through LDS.  A tile
@@ -23,8 +22,7 @@
 namespace qlora {
 namespace {
 
-constexpr int KT = 128;     // columns of a tile
-constexpr int kStages = 4;  // of the tokens' ring
+constexpr int KT = 128;  // columns of a tile
 
 // Until at most `vm` vector-memory operations of the wave are outstanding, and
 // no LDS operation.
@@ -42,53 +40,18 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-z)) * u;
 }
 
-// The share of K and of the output that a block has.  The first `full` blocks
-// have a whole tile each; the tail_q tiles behind them are split tail_s ways
-// over K, and their sums go to the workspace.
-struct Part {
-  int m, n;  // tile
-  int tail;  // of the tail's tiles, or -1
-  int z, nz;
-};
-// Neighbouring ranks are on one XCD, whose L2 then holds what they share
-// (blocks go to the eight XCDs in turn).
-__device__ __forceinline__ uint32_t xcd_rank(uint32_t id, uint32_t total) {
+// The tile of a block.  Blocks go to the eight XCDs in turn; neighbouring ranks
+// are made to be on one, whose L2 then holds what they share.  Ranks walk bands
+// of 1024 tokens, a column of tiles of the band at a time.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t total, uint32_t m_tiles,
+                                        uint32_t n_tiles, uint32_t band, uint32_t& m, uint32_t& n) {
   const uint32_t xcd = id % 8, per = total / 8, extra = total % 8;
-  return xcd * per + (xcd < extra ? xcd : extra) + id / 8;
+  const uint32_t rank = xcd * per + min(xcd, extra) + id / 8;
+  const uint32_t span = band * n_tiles, g = rank / span, w = rank - g * span;
+  const uint32_t gm = min(m_tiles - band * g, band);
+  n = w / gm;
+  m = band * g + (w - n * gm);
 }
-// Ranks walk groups of four rows of tiles, a column of the group at a time.
-__device__ __forceinline__ void tile_at(uint32_t rank, uint32_t m_tiles, uint32_t n_tiles, int& m,
-                                        int& n) {
-  const uint32_t span = 4 * n_tiles, g = rank / span, w = rank - g * span;
-  const uint32_t gm = min(m_tiles - 4 * g, 4u);
-  n = (int)(w / gm);
-  m = (int)(4 * g + (w - (uint32_t)n * gm));
-}
-__device__ __forceinline__ Part part_of(uint32_t id, uint32_t m_tiles, uint32_t n_tiles,
-                                        const I8GemmPlan& p) {
-  Part o;
-  uint32_t rank;
-  if (id < (uint32_t)p.full) {
-    rank = xcd_rank(id, p.full);
-    o.tail = -1;
-    o.z = 0;
-    o.nz = 1;
-  } else {
-    const uint32_t r = xcd_rank(id - p.full, p.tail_q * p.tail_s);
-    o.z = (int)(r / p.tail_q);
-    o.nz = p.tail_s;
-    o.tail = (int)(r - o.z * p.tail_q);
-    rank = p.full + o.tail;
-  }
-  tile_at(rank, m_tiles, n_tiles, o.m, o.n);
-  return o;
-}
-
-struct GemmArg {
-  I8LinearArg a;
-  I8GemmPlan plan;
-  i32x4_t* part;  // [tail_s][tail_q][wave][JT][NI][4][64]
-};
 
 // A wave's outputs: RO rows from n0 on of the 32 J tokens from m0 on.  All of
 // them are scaled into the wave's LDS first, and go out from there in a loop,
@@ -167,27 +130,43 @@ struct Outputs {
   }
 };
 
-template <class DT, int NI, int JT, int G>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, JT == 8 ? 1 : 2)))
-void gemm_i8_kernel(GemmArg g) {
+// KS: groups of four waves that each take a share of K.  WPE: waves of a SIMD
+// that the registers are to leave room for.
+template <class DT, int NI, int JT, int G, int KS, int WPE>
+__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(1, WPE)))
+void gemm_i8_kernel(I8LinearArg p) {
   using S = Outputs<DT, NI, G, JT>;
   constexpr int TM = 32 * JT, RO = S::RO, TN = 4 * RO;
+  constexpr int ST = 4;                // stages of the tokens' ring
+  constexpr int WD = 2;                // tiles of K whose weights are held or on their way
   constexpr int XR = JT;               // DMA instructions of a wave a tile
   constexpr int LC = 4 * NI;           // loads of weights a tile
   constexpr int XST = TM * KT;         // bytes of a stage
   constexpr int SLOTS = NI * JT;       // matrix instructions a step
   constexpr int DP = 4 * SLOTS / XR;   // of these from one DMA to the next
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * XST > 4 * S::kBytes ? kStages * XST : 4 * S::kBytes];
-  const I8LinearArg& p = g.a;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int kSums = 4 * JT * NI * 4 * 64;  // of a share, in 16 bytes
+  constexpr int kRings = KS * ST * XST, kJoin = (KS - 1) * kSums * 16, kOut = 4 * S::kBytes;
+  constexpr int kLds = kRings > kJoin ? (kRings > kOut ? kRings : kOut) : (kJoin > kOut ? kJoin : kOut);
+  __shared__ __attribute__((aligned(16))) uint8_t lds_all[kLds];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = wv % 4, share = wv / 4;
   const int lr = lane & 31, lg = lane >> 5;
+  uint8_t* const lds = lds_all + share * (ST * XST);
   const int64_t Kp = i8_padded(p.K), n_panels = (p.N + 15) / 16;
-  const uint32_t m_tiles = (uint32_t)((p.M + TM - 1) / TM), n_tiles = (uint32_t)((p.N + TN - 1) / TN);
-  const Part w = part_of(blockIdx.x, m_tiles, n_tiles, g.plan);
-  const int64_t m0 = (int64_t)w.m * TM, n0 = (int64_t)w.n * TN;
-  const int nkt = (int)(Kp / KT), pairs = (nkt + 1) / 2;
-  const int kt0 = 2 * (int)((uint32_t)(pairs * w.z) / w.nz),
-            kt1 = min(nkt, 2 * (int)((uint32_t)(pairs * (w.z + 1)) / w.nz));
+  uint32_t mt, nt;
+  tile_of(blockIdx.x, gridDim.x, (uint32_t)((p.M + TM - 1) / TM), (uint32_t)((p.N + TN - 1) / TN),
+          1024 / TM, mt, nt);
+  const int64_t m0 = (int64_t)mt * TM, n0 = (int64_t)nt * TN;
+  // x of tile kt + 2 has to be there at the end of iteration kt, and is when
+  // no more operations are outstanding than came behind it: those of ST - 3
+  // iterations and the last weights of its own, or in the first iterations
+  // those of the prologue.
+  constexpr int kSteady = (ST - 3) * (XR + LC) + NI, kFirst = (ST - 3) * XR + WD * LC;
+  constexpr int kWait = kSteady < kFirst ? kSteady : kFirst;
+  static_assert(kWait < 64 && ST >= 4, "outstanding operations of a wave");
+  // Every share has the same number of tiles, for they meet at barriers.
+  const int nkt = (int)(Kp / KT), each = (nkt + WD * KS - 1) / (WD * KS) * WD;
+  const int kt0 = each * share, kt1 = kt0 + each;
 
   // Operands of a weight: lane l has row l % 32 and 16 columns of a step of
   // 32.  Panels past the end read as zeros (the range check covers the lane's
@@ -201,10 +180,9 @@ void gemm_i8_kernel(GemmArg g) {
 #pragma unroll
   for (int i = 0; i < NI; ++i)
     wo[i] = (wave * (RO / 16) + (G == 2 ? 0 : 2 * i) + (lr >> 4)) * panel + lg * 256 + (lr & 15) * 16;
-  // Tiles are worked on in pairs; weights of one past the last are zeros (a
-  // buffer of no bytes).
+  // Weights of tiles past the last are zeros (a buffer of no bytes).
   auto load_w = [&](int kt, int i, int kk) -> u32x4_t {
-    const auto buf = make_rsrc(G == 2 && i == 1 ? w1 : w0, kt < kt1 ? held : 0);
+    const auto buf = make_rsrc(G == 2 && i == 1 ? w1 : w0, kt < nkt ? held : 0);
     return buffer_load16(buf, wo[i] + (kk >> 1) * 1024 + (kk & 1) * 512,
                          (uint32_t)kt * (2 * kI8Tile));
   };
@@ -236,30 +214,30 @@ void gemm_i8_kernel(GemmArg g) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[j][i][v] = 0;
 
-  if (kt0 < kt1) {
-    const int last = kt1 - 1;
-    auto cl = [&](int kt) { return kt < last ? kt : last; };
-    u32x4_t W[2][4][NI], X[2][JT];
-    // x of the first two tiles, weights of the first, then as in the loop
+  {
+    auto cl = [&](int kt) { return kt < nkt ? kt : nkt - 1; };
+    u32x4_t W[WD][4][NI], X[2][JT];
+    auto load_tile = [&](int kt, int at) {
 #pragma unroll
-    for (int q = 0; q < XR; ++q) dma_x(lds, kt0, q);
+      for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-    for (int q = 0; q < XR; ++q) dma_x(lds + XST, cl(kt0 + 1), q);
-    __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < NI; ++i) W[at][kk][i] = load_w(kt, i, kk);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto dma_tile = [&](int kt, int at) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+      for (int q = 0; q < XR; ++q) dma_x(lds + at * XST, cl(kt), q);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // x of the first two tiles, weights of the first, then the rest
+    dma_tile(kt0, 0);
+    dma_tile(kt0 + 1, 1);
+    load_tile(kt0, 0);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) W[0][kk][i] = load_w(kt0, i, kk);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int d = 2; d < ST - 1; ++d) dma_tile(kt0 + d, d);
 #pragma unroll
-    for (int q = 0; q < XR; ++q) dma_x(lds + 2 * XST, cl(kt0 + 2), q);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) W[1][kk][i] = load_w(kt0 + 1, i, kk);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_imm(XR + 2 * LC));
+    for (int d = 1; d < WD; ++d) load_tile(kt0 + d, d);
+    __builtin_amdgcn_s_waitcnt(wait_imm((ST - 3) * XR + WD * LC));
     __builtin_amdgcn_s_barrier();
 #pragma unroll
     for (int j = 0; j < JT; ++j) X[0][j] = read_x(lds, 0, j);
@@ -280,155 +258,148 @@ void gemm_i8_kernel(GemmArg g) {
           if (i == NI - 1)
             X[(kk + 1) & 1][j] = kk < 3 ? read_x(now, kk + 1, j) : read_x(next, 0, j);
           const int slot = SLOTS * kk + s;
-          if (slot % DP == DP - 1) dma_x(fill, cl(kt + 3), slot / DP);
+          if (slot % DP == DP - 1) dma_x(fill, cl(kt + ST - 1), slot / DP);
           // the registers of the step before are free
-          if (kk > 0 && s % (SLOTS / NI) == SLOTS / NI / 2 - 1)
-            W[ph][kk - 1][s / (SLOTS / NI)] = load_w(kt + 2, s / (SLOTS / NI), kk - 1);
+          if (kk > 0 && s % JT == (JT - 1) / 2)
+            W[ph][kk - 1][s / JT] = load_w(kt + WD, s / JT, kk - 1);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
 #pragma unroll
-      for (int i = 0; i < NI; ++i) W[ph][3][i] = load_w(kt + 2, i, 3);
+      for (int i = 0; i < NI; ++i) W[ph][3][i] = load_w(kt + WD, i, 3);
       __builtin_amdgcn_sched_barrier(0);
-      // x of tile kt + 2: all that the last iteration asked for but its last
-      // weights
-      __builtin_amdgcn_s_waitcnt(wait_imm(XR + LC + NI));
+      __builtin_amdgcn_s_waitcnt(wait_imm(kWait));
       __builtin_amdgcn_s_barrier();
     };
-    int stage = 0, kt = kt0;
-    auto at = [&](int d) { return lds + ((stage + d) & (kStages - 1)) * XST; };
-    for (; kt < kt1; kt += 2, stage += 2) {
-      iteration(kt, std::integral_constant<int, 0>(), at(0), at(1), at(3));
-      iteration(kt + 1, std::integral_constant<int, 1>(), at(1), at(2), at(4));
+    int stage = 0;
+    auto at = [&](int d) { return lds + (stage + d < ST ? stage + d : stage + d - ST) * XST; };
+    auto step = [&](int kt, auto phase) {
+      iteration(kt, phase, at(0), at(1), at(ST - 1));
+      stage = stage + 1 < ST ? stage + 1 : 0;
+    };
+    for (int kt = kt0; kt < kt1; kt += WD) {
+      step(kt, std::integral_constant<int, 0>());
+      step(kt + 1, std::integral_constant<int, 1>());
+      if constexpr (WD == 4) {
+        step(kt + 2, std::integral_constant<int, 2>());
+        step(kt + 3, std::integral_constant<int, 3>());
+      }
     }
     // what was asked for past the end is still on its way to LDS
     __builtin_amdgcn_s_waitcnt(wait_imm(0));
   }
   __syncthreads();
-  if (w.tail >= 0) {
-    i32x4_t* o = g.part +
-                 ((int64_t)(w.z * g.plan.tail_q + w.tail) * 4 + wave) * (JT * NI * 4 * 64) + lane;
+  if constexpr (KS > 1) {
+    // the other shares' sums come to the first
+    i32x4_t* const sums = reinterpret_cast<i32x4_t*>(lds_all) + wave * (kSums / 4) + lane;
+    if (share > 0) {
+      i32x4_t* const mine = sums + (share - 1) * kSums;
 #pragma unroll
-    for (int j = 0; j < JT; ++j)
+      for (int j = 0; j < JT; ++j)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        i32x16_t a = acc[j][i];
-        asm volatile("" : "+a"(a));
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          o[((j * NI + i) * 4 + q) * 64] =
-              i32x4_t{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
-      }
+          for (int q = 0; q < 4; ++q)
+            mine[((j * NI + i) * 4 + q) * 64] = i32x4_t{acc[j][i][4 * q], acc[j][i][4 * q + 1],
+                                                        acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+    }
+    __syncthreads();
+    if (share > 0) return;
+#pragma unroll
+    for (int k = 0; k < KS - 1; ++k)
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const i32x4_t v = sums[k * kSums + ((j * NI + i) * 4 + q) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][i][4 * q + e] += v[e];
+          }
+    // a wave's outputs go where only its own sums were: no wait
+    static_assert(S::kBytes <= kSums / 4 * 16, "the wave's own place");
+    S::run(acc, p, n0 + wave * RO, m0, lds_all + wave * (kSums / 4 * 16), lane);
   } else {
     S::run(acc, p, n0 + wave * RO, m0, lds + wave * S::kBytes, lane);
   }
 }
 
-// The tail's sums over its splits: a wave has 32 tokens of a wave's tile.
-template <class DT, int NI, int JT, int G>
-__global__ __launch_bounds__(256) void join_i8_kernel(GemmArg g) {
-  using S = Outputs<DT, NI, G, 1>;
-  constexpr int TM = 32 * JT, RO = S::RO, TN = 4 * RO;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * S::kBytes];
-  const I8LinearArg& p = g.a;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t piece = blockIdx.x * 4 + wave;  // [tail][wave][j]
-  const int owner = piece / JT % 4, j = piece % JT;
-  int m, n;
-  tile_at((uint32_t)g.plan.full + piece / (4 * JT), (uint32_t)((p.M + TM - 1) / TM),
-          (uint32_t)((p.N + TN - 1) / TN), m, n);
-  const int64_t n0 = (int64_t)n * TN + owner * RO, m0 = (int64_t)m * TM + 32 * j;
-  if (n0 >= p.N || m0 >= p.M) return;
-  const int64_t stride = (int64_t)g.plan.tail_q * 4 * JT * NI * 4 * 64;
-  const i32x4_t* src = g.part + (int64_t)piece * (NI * 4 * 64) + lane;
-  i32x16_t acc[1][NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) acc[0][i][v] = 0;
-  for (int z = 0; z < g.plan.tail_s; ++z, src += stride)
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const i32x4_t v = src[(i * 4 + q) * 64];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[0][i][4 * q + e] += v[e];
-      }
-  S::run(acc, p, n0, m0, lds + wave * S::kBytes, lane);
+template <class DT, int NI, int JT, int G, int KS, int WPE>
+void go(const I8LinearArg& p, hipStream_t s) {
+  constexpr int TM = 32 * JT, TN = G == 2 ? 128 : 128 * NI;
+  const int64_t blocks = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
+  gemm_i8_kernel<DT, NI, JT, G, KS, WPE><<<dim3((unsigned)blocks), 256 * KS, 0, s>>>(p);
 }
 
-template <class DT, int NI, int JT, int G>
-void go(const GemmArg& g, hipStream_t s) {
-  const int64_t blocks = g.plan.full + (int64_t)g.plan.tail_q * g.plan.tail_s;
-  gemm_i8_kernel<DT, NI, JT, G><<<dim3((unsigned)blocks), 256, 0, s>>>(g);
-  if (g.plan.tail_q > 0)
-    join_i8_kernel<DT, NI, JT, G><<<dim3((unsigned)(g.plan.tail_q * JT)), 256, 0, s>>>(g);
+// Which tile.  What a tile of K (128 columns) takes, in us, as measured (gfx950,
+// 2.35 GHz while the chip is not at its power limit): `busy` for each block that
+// a CU has when all have some, `alone` for a block when most CUs have none.  Of
+// a call with B blocks that is the larger of busy B / 256 and alone ceil(B /
+// 256), for the CU that has most.  Small tiles give more blocks, large ones read
+// less: 501 tokens, N 4096, K 4096 take 13.2 us with 64 x 128, 15.7 with 128 x
+// 128, 16.7 with 32 x 128 and 23.9 with 128 x 256; 1000 tokens, N and K 8192 take
+// 85, 64, 120 and 60.  A tile of 256 x 256 gained 2 % at 8192^3 and nothing at
+// 4096 x 22016 x 8192; splitting K over blocks, with a join in a second launch,
+// gained 3 % in the latter's last round and lost elsewhere (501 tokens 22 us, 2048
+// tokens of N 4096, K 11008 92 against 85).
+struct Tile {
+  int tm, tn;
+  float busy, alone;
+};
+constexpr Tile kPlain[] = {{32, 128, 0.225f, 0.12f}, {64, 128, 0.27f, 0.2f},
+                           {128, 128, 0.48f, 0.33f}, {128, 256, 0.83f, 0.59f}};
+constexpr Tile kGated[] = {{32, 128, 0.43f, 0.25f}, {64, 128, 0.52f, 0.35f}, {128, 128, 0.88f, 0.59f}};
+template <int C>
+int best_of(const Tile (&tiles)[C], int64_t M, int64_t N) {
+  int best = 0;
+  float least = 0.0f;
+  for (int i = 0; i < C; ++i) {
+    const Tile& t = tiles[i];
+    const int64_t blocks = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn);
+    const float a = t.busy * (float)blocks / 256.0f, b = t.alone * (float)((blocks + 255) / 256);
+    const float time = a > b ? a : b;
+    if (i == 0 || time < least) best = i, least = time;
+  }
+  return best;
 }
 
 template <class DT, int G>
-void pick(const GemmArg& g, hipStream_t s) {
-  const I8GemmPlan& p = g.plan;
-  if (G == 2 || p.tn == 256) {
-    if (p.tm == 256) return go<DT, 2, 8, G>(g, s);
-    if (p.tm == 128) return go<DT, 2, 4, G>(g, s);
-    return go<DT, 2, 2, G>(g, s);
-  }
-  if constexpr (G == 1) {
-    if (p.tm == 128) return go<DT, 1, 4, G>(g, s);
-    return go<DT, 1, 2, G>(g, s);
+void pick(const I8LinearArg& p, hipStream_t s) {
+  if constexpr (G == 2) {
+    switch (best_of(kGated, p.M, p.N)) {
+      case 0: return go<DT, 2, 1, 2, 1, 2>(p, s);
+      case 1: return go<DT, 2, 2, 2, 1, 2>(p, s);
+      default: return go<DT, 2, 4, 2, 1, 2>(p, s);
+    }
+  } else {
+    switch (best_of(kPlain, p.M, p.N)) {
+      case 0:
+        // two shares of K where a CU has one block (64 tokens, N and K 8192:
+        // 19.1 us with one, 16.4 with two, 17.4 with four; 501 tokens, N 4096,
+        // two blocks a CU: 16.7, 16.9, 19.9)
+        if (((p.M + 31) / 32) * ((p.N + 127) / 128) <= 256) return go<DT, 1, 1, 1, 2, 4>(p, s);
+        return go<DT, 1, 1, 1, 1, 4>(p, s);
+      case 1: return go<DT, 1, 2, 1, 1, 4>(p, s);
+      case 2: return go<DT, 1, 4, 1, 1, 2>(p, s);
+      default: return go<DT, 2, 4, 1, 1, 2>(p, s);
+    }
   }
 }
 
 }  // namespace
 
-I8GemmPlan gemm_i8_plan(int64_t M, int64_t N, int64_t K, bool gated) {
-  const int64_t nkt = i8_padded(K) / KT;
-  I8GemmPlan best{};
-  double best_t = 1e300;
-  for (int tm = 256; tm >= 128; tm /= 2) {
-    const int tn = gated ? 128 : 256;
-    const int64_t tiles = ((M + tm - 1) / tm) * ((N + tn - 1) / tn);
-    const double tile_t = (tm == 256 ? 1.0 : 0.6) * nkt;
-    I8GemmPlan p{tm, tn, (int)tiles, 0, 1};
-    const int64_t q = tiles % 256;
-    double t = (double)((tiles + 255) / 256) * tile_t;
-    if (q > 0) {
-      int64_t s = 256 / q;
-      if (s > nkt / 2) s = nkt / 2;
-      if (s > 16) s = 16;
-      if (s >= 2) {
-        p.full = (int)(tiles - q);
-        p.tail_q = (int)q;
-        p.tail_s = (int)s;
-        t = ((double)(tiles / 256) + 1.0 / s) * tile_t + 4 + (double)(s * q * tm) / 16384;
-      }
-    }
-    if (t < best_t) {
-      best_t = t;
-      best = p;
-    }
-  }
-  return best;
-}
-
-size_t gemm_i8_workspace(const I8GemmPlan& p, bool gated) {
-  return (size_t)p.tail_q * (p.tail_q ? p.tail_s : 0) * p.tm * p.tn * (gated ? 2 : 1) * 4;
-}
-
-hipError_t launch_gemm_i8(const I8LinearArg& p, const I8GemmPlan& plan, int32_t* workspace,
-                          bool f16, hipStream_t s) {
-  const GemmArg g{p, plan, reinterpret_cast<i32x4_t*>(workspace)};
+hipError_t launch_gemm_i8(const I8LinearArg& p, bool f16, hipStream_t s) {
   if (p.tiles[1]) {
     if (f16)
-      pick<F16T, 2>(g, s);
+      pick<F16T, 2>(p, s);
     else
-      pick<Bf16T, 2>(g, s);
+      pick<Bf16T, 2>(p, s);
   } else {
     if (f16)
-      pick<F16T, 1>(g, s);
+      pick<F16T, 1>(p, s);
     else
-      pick<Bf16T, 1>(g, s);
+      pick<Bf16T, 1>(p, s);
   }
   return hipGetLastError();
 }

@@ -285,18 +285,8 @@ struct I8LinearArg {
   int act;  // kI8Silu, kI8Gelu
 };
 constexpr int kI8Silu = 0, kI8Gelu = 1;
-// i8_gemm.hip -- the form for many tokens: blocks with tiles of tm tokens and
-// tn rows; the first `full` tiles run whole, the tail_q behind them are split
-// tail_s ways over K.
-struct I8GemmPlan {
-  int tm, tn;
-  int full, tail_q, tail_s;
-};
-I8GemmPlan gemm_i8_plan(int64_t M, int64_t N, int64_t K, bool gated);
-size_t gemm_i8_workspace(const I8GemmPlan& p, bool gated);
-hipError_t launch_gemm_i8(const I8LinearArg& p, const I8GemmPlan& plan, int32_t* workspace,
-                          bool f16, hipStream_t s);
-size_t linear_i8_workspace(int64_t M, int64_t N, int64_t K, bool gated);
-hipError_t launch_linear_i8(const I8LinearArg& p, int32_t* workspace, bool f16, hipStream_t s);
+hipError_t launch_linear_i8(const I8LinearArg& p, bool f16, hipStream_t s);
+// i8_gemm.hip -- its form for many tokens
+hipError_t launch_gemm_i8(const I8LinearArg& p, bool f16, hipStream_t s);
 
 }  // namespace qlora

@@ -13,14 +13,12 @@ from __future__ import annotations
 
 import torch
 
-from . import _lib
 from ._lib import I8TokensStruct, I8WeightStruct
 from .u4 import _16BIT, _call, _dense, _need
 
 PAD = 128
 ACTS = {"silu": 0, "gelu": 1}
-_i8, _f32, _u8 = torch.int8, torch.float32, torch.uint8
-_most = None
+_i8, _f32 = torch.int8, torch.float32
 
 
 def _padded(K: int) -> int:
@@ -207,18 +205,12 @@ def rms_norm_i8(x, weight, eps: float, residual=None, h=None, out=None):
 # products
 # ---------------------------------------------------------------------------
 
-def linear_i8_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
-    for n, v in (("M", M), ("N", N), ("K", K)):
-        _need(-2 ** 63 <= v < 2 ** 63, f"{n} {v} is out of range")
-    return int(_lib.lib().qlora_linear_i8_workspace_bytes(M, N, K, 1 if gated else 0))
-
-
-def _product(name, ws, more, x, y, dtype, workspace):
+def _product(name, ws, more, x, y, dtype):
     """The call ``name`` of the weights ``ws`` and the arguments ``more``."""
     w = ws[0]
-    N, K, index, M = w.N, w.K, w.index, x.M
-    if x.K != K or x.index != index:
-        raise ValueError(f"tokens of {K} values on GPU {index} are needed, got {x.K} on {x.device}")
+    N, index, M = w.N, w.index, x.M
+    if x.K != w.K or x.index != index:
+        raise ValueError(f"tokens of {w.K} values on GPU {index} are needed, got {x.K} on {x.device}")
     args = [v.now() for v in ws]
     tokens = x.now()
     if dtype is None:
@@ -230,30 +222,17 @@ def _product(name, ws, more, x, y, dtype, workspace):
         ldy = N
     else:
         ldy = _rows(y, "y", dtype, (M, N), index)
-    global _most
-    if _most is None:
-        _most = _lib.lib().qlora_linear_i8_workspace_bytes
-    wp = None
-    if workspace is None:
-        need = _most(M, N, K, len(ws) - 1)
-        if need:
-            workspace = torch.empty(need, dtype=_u8, device=x.device)
-            wp = workspace.data_ptr()
-    else:
-        _dense(workspace, "workspace", _u8, index)
-        need, wp = workspace.numel(), workspace.data_ptr()
-    _call(name, dtype, index, *args, *more, tokens, y.data_ptr(), ldy, wp, need)
+    _call(name, dtype, index, *args, *more, tokens, y.data_ptr(), ldy)
     return y
 
 
-def linear_i8_fwd(iw: I8Weight, x: I8Tokens, y=None, dtype=None, workspace=None):
+def linear_i8_fwd(iw: I8Weight, x: I8Tokens, y=None, dtype=None):
     """y = x . W^T of 8-bit tokens and an 8-bit weight, [M, N] in ``dtype``
     (bf16 or fp16; default: y's type, or bf16); y may have strided rows."""
-    return _product("qlora_linear_i8_fwd", (iw,), (), x, y, dtype, workspace)
+    return _product("qlora_linear_i8_fwd", (iw,), (), x, y, dtype)
 
 
-def gated_i8_fwd(gate: I8Weight, up: I8Weight, x: I8Tokens, act: str = "silu", y=None, dtype=None,
-                 workspace=None):
+def gated_i8_fwd(gate: I8Weight, up: I8Weight, x: I8Tokens, act: str = "silu", y=None, dtype=None):
     """y = act(x . gate^T) * (x . up^T), [M, N], in one pass; ``act`` is
     "silu" or "gelu" (its tanh form).  Other arguments as
     :func:`linear_i8_fwd`."""
@@ -262,4 +241,4 @@ def gated_i8_fwd(gate: I8Weight, up: I8Weight, x: I8Tokens, act: str = "silu", y
     if up.N != gate.N or up.K != gate.K or up.index != gate.index:
         raise ValueError(f"up: [{gate.N}, {gate.K}] on GPU {gate.index} is needed, got "
                          f"[{up.N}, {up.K}] on {up.device}")
-    return _product("qlora_gated_i8_fwd", (gate, up), (ACTS[act],), x, y, dtype, workspace)
+    return _product("qlora_gated_i8_fwd", (gate, up), (ACTS[act],), x, y, dtype)

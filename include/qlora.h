@@ -622,31 +622,24 @@ int qlora_rms_norm_i8_f16(const uint16_t* x, int64_t ldx, const uint16_t* residu
  * has to be w->K (EINVAL).  The sums of the codes' products are exact (int32);
  * y = sum * sw[n] * sx[m] in fp32, left to right, rounded once to 16 bits.
  * The same bits on every run and for every M.  M up to 2^20 - 16, and M * N
- * up to 2^34 (ESHAPE).
- * workspace (256-byte aligned): at least
- * qlora_linear_i8_workspace_bytes(M, N, K, 0) bytes, or NULL where that is 0
- * (also its answer for an invalid shape); it is written before it is read.  */
-size_t qlora_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t gated);
+ * up to 2^34 (ESHAPE).  No workspace.                                        */
 int qlora_linear_i8_fwd(const qlora_i8_weight* w, const qlora_i8_tokens* x, uint16_t* y,
-                        int64_t ldy, void* workspace, size_t ws_bytes, void* stream);
+                        int64_t ldy, void* stream);
 int qlora_linear_i8_fwd_f16(const qlora_i8_weight* w, const qlora_i8_tokens* x, uint16_t* y,
-                            int64_t ldy, void* workspace, size_t ws_bytes, void* stream);
+                            int64_t ldy, void* stream);
 
 /* The gated half of an MLP: y = act(g) * u with g = x . gate^T and
  * u = x . up^T (weights of one shape, EINVAL), in one pass; g and u are fp32
  * and never rounded to 16 bits.  act (ENOTSUP for others):
  *   QLORA_ACT_SILU  g / (1 + exp(-g))
  *   QLORA_ACT_GELU  the tanh form, g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
- * Other arguments as above; workspace
- * qlora_linear_i8_workspace_bytes(M, N, K, 1).                              */
+ * Other arguments as above.                                                  */
 #define QLORA_ACT_SILU 0
 #define QLORA_ACT_GELU 1
 int qlora_gated_i8_fwd(const qlora_i8_weight* gate, const qlora_i8_weight* up, int32_t act,
-                       const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* workspace,
-                       size_t ws_bytes, void* stream);
+                       const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* stream);
 int qlora_gated_i8_fwd_f16(const qlora_i8_weight* gate, const qlora_i8_weight* up, int32_t act,
-                           const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* workspace,
-                           size_t ws_bytes, void* stream);
+                           const qlora_i8_tokens* x, uint16_t* y, int64_t ldy, void* stream);
 
 /* Workspace bytes for op 0 (forward) or 1 (backward) of the NF4 layer,
  * op 2 (forward) or 3 (backward) of the bf16-weight layer, op 4 (forward)
