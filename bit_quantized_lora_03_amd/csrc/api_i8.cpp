@@ -16,12 +16,11 @@ namespace {
 // No sum of K products of two codes (-128 among them, which no quantiser
 // writes) passes 2^31.
 constexpr int64_t kMaxK = (int64_t{1} << 17) - qlora::kI8Pad;
-// A launch holds below 2^32 threads along x: 1024 for 16 rows.
-constexpr int64_t kMaxN = (int64_t{1} << 26) - 16;
+// A launch holds below 2^32 threads along x: the quantiser's 1024 for 4 rows.
+constexpr int64_t kMaxN = (int64_t{1} << 24) - 64;
 constexpr int64_t kMaxM = int64_t{1} << 30;
-// Tokens of a product: its grid has tiles of 64 tokens and 64 rows below 2^22,
-// and of 64 tokens below 2^16 along y.
-constexpr int64_t kMaxLinearM = int64_t{65535} * 16;
+// Tokens of a product: their scales have 32-bit offsets.
+constexpr int64_t kMaxLinearM = int64_t{1} << 28;
 constexpr int64_t kMaxStride = (int64_t{1} << 31) - 1;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -176,6 +175,7 @@ int linear(const qlora_i8_weight* w, const qlora_i8_weight* up, bool gated, int3
     if (x->K != w->K) return QLORA_EINVAL;
     if (x->M == 0) return QLORA_OK;
     if (!y || ldy < w->N) return QLORA_EINVAL;
+    // a grid has at most two blocks, of 256 threads, for each 64 x 64 outputs
     if (ldy > kMaxStride || x->M > kMaxLinearM ||
         ((x->M + 63) / 64) * ((w->N + 63) / 64) >= (int64_t{1} << 22))
       return QLORA_ESHAPE;

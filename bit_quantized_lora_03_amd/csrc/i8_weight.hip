@@ -1,10 +1,12 @@
 // A weight in the 8-bit row format and its tiles (i8_common.h): the quantiser
 // of fp32 rows and what they stand for.
 //
-// A block of sixteen waves has a panel of 16 rows, a wave a row.  The row is
-// read twice, for its largest magnitude and for its codes.  Codes
-// of 1024 columns of the panel go through LDS into the tiles' order, which is
-// one run of 16 KiB, so every store is whole lines.
+// Bound by HBM: 4 bytes of a value in, one out.  A row of up to 16384 values
+// stays in registers between the search for its largest magnitude and its
+// codes: a block of sixteen waves has 16, 8 or 4 rows, by their length, and a
+// lane 64 values.  Longer rows are read twice, a wave a row.  Codes go through
+// LDS into the tiles' order, 16 KiB at a time, so stores are runs of a block's
+// rows (256, 128 or 64 bytes).
 
 #include "i8_common.h"
 #include "launch.h"
@@ -68,6 +70,63 @@ __global__ __launch_bounds__(1024) void quantize_i8_kernel(const float* __restri
   }
 }
 
+// WR: waves of a row.
+template <int WR>
+__global__ __launch_bounds__(1024) void quantize_rows_i8_kernel(const float* __restrict__ w,
+                                                                int N, int K,
+                                                                int8_t* __restrict__ tiles,
+                                                                float* __restrict__ scales) {
+  constexpr int R = 16 / WR;            // rows of the block
+  constexpr int COLS = 1024 * WR;       // columns at a time
+  constexpr int LD = COLS + 16;         // bytes of a row in LDS
+  __shared__ __attribute__((aligned(16))) int8_t lds[2][R * LD];
+  __shared__ uint32_t tops[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = wave / WR, part = wave % WR;
+  const int n = blockIdx.x * R + r, Kp = (int)i8_padded(K);
+  const bool row = n < N;
+  const float* src = w + (int64_t)(row ? n : N - 1) * K;
+  f32x4_t v[16];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = load4(src, (i * WR + part) * 256 + 4 * lane, K);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+  if constexpr (WR > 1) {
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < WR; ++q) top = max(top, tops[r * WR + q]);
+  }
+  const I8Row code = i8_row(__uint_as_float(top), 1.0, top < 0x7F800000u);
+  if (row && lane == 0 && part == 0) scales[n] = code.s;
+  int8_t* dst = tiles + (int64_t)(blockIdx.x / WR) * 16 * Kp + (blockIdx.x % WR) * (16 * R);
+  // thread t stores 16 columns of row t % R
+  const int t = threadIdx.x, tr = t % R, piece = t / R;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (g * COLS >= Kp) break;
+    int8_t* at = &lds[g & 1][r * LD + part * 256 + 4 * lane];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        c |= ((uint32_t)i8_code(code, v[4 * g + i][j]) & 0xFFu) << (8 * j);
+      *reinterpret_cast<uint32_t*>(at + i * (256 * WR)) = row ? c : 0u;
+    }
+    __syncthreads();
+    const int col = g * COLS + 16 * piece;
+    if (col < Kp)
+      *reinterpret_cast<u32x4_t*>(dst + (col >> 6) * kI8Tile + ((col >> 4) & 3) * 256 + 16 * tr) =
+          *reinterpret_cast<const u32x4_t*>(&lds[g & 1][tr * LD + 16 * piece]);
+  }
+}
+
 // A wave has a row of the panel, a lane 16 columns of it: the sixteen waves
 // read the lines of a tile together.
 template <class DT>
@@ -100,7 +159,15 @@ __global__ __launch_bounds__(1024) void dequantize_i8_kernel(const int8_t* __res
 
 hipError_t launch_quantize_i8(const float* w, int64_t N, int64_t K, int8_t* tiles, float* scales,
                               hipStream_t s) {
-  quantize_i8_kernel<<<dim3((unsigned)((N + 15) / 16)), 1024, 0, s>>>(w, N, K, tiles, scales);
+  const unsigned panels = (unsigned)((N + 15) / 16);
+  if (K <= 4096)
+    quantize_rows_i8_kernel<1><<<dim3(panels), 1024, 0, s>>>(w, (int)N, (int)K, tiles, scales);
+  else if (K <= 8192)
+    quantize_rows_i8_kernel<2><<<dim3(2 * panels), 1024, 0, s>>>(w, (int)N, (int)K, tiles, scales);
+  else if (K <= 16384)
+    quantize_rows_i8_kernel<4><<<dim3(4 * panels), 1024, 0, s>>>(w, (int)N, (int)K, tiles, scales);
+  else
+    quantize_i8_kernel<<<dim3(panels), 1024, 0, s>>>(w, N, K, tiles, scales);
   return hipGetLastError();
 }
 

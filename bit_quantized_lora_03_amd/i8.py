@@ -25,6 +25,12 @@ def _padded(K: int) -> int:
     return (K + PAD - 1) // PAD * PAD
 
 
+def _held(what, index, first, scales):
+    """Refuses tensors that are not int8 and fp32, dense and on one GPU."""
+    _dense(first, what, _i8)
+    _dense(scales, "scales", _f32, index)
+
+
 class I8Weight:
     """A weight [N, K] in the 8-bit row format: ``tiles`` int8
     [ceil(N / 16), Kp / 64, 4, 16, 16] with Kp = K rounded up to 128 (sixteen
@@ -34,11 +40,13 @@ class I8Weight:
     __slots__ = ("tiles", "scales", "N", "K", "index", "struct", "at")
 
     def __init__(self, tiles, scales, N: int, K: int):
-        _dense(tiles, "tiles", _i8)
         index = tiles.get_device()
-        _dense(scales, "scales", _f32, index)
-        if N < 1 or K < 1 or tuple(scales.shape) != (N,) or \
-                tuple(tiles.shape) != ((N + 15) // 16, _padded(K) // 64, 4, 16, 16):
+        if tiles.dtype is not _i8 or scales.dtype is not _f32 or index < 0 or \
+                scales.get_device() != index or not tiles.is_contiguous() or \
+                not scales.is_contiguous():
+            _held("tiles", index, tiles, scales)
+        if N < 1 or K < 1 or scales.shape != (N,) or \
+                tiles.shape != ((N + 15) // 16, (K + 127) // 128 * 2, 4, 16, 16):
             raise ValueError(f"tiles [{(N + 15) // 16}, {_padded(K) // 64}, 4, 16, 16] and scales "
                              f"[{N}] are needed for a weight [{N}, {K}]")
         self.tiles, self.scales, self.N, self.K, self.index = tiles, scales, N, K, index
@@ -67,11 +75,14 @@ class I8Tokens:
     __slots__ = ("codes", "scales", "M", "K", "index", "struct", "at")
 
     def __init__(self, codes, scales, K: int):
-        _dense(codes, "codes", _i8)
         index = codes.get_device()
-        _dense(scales, "scales", _f32, index)
+        if codes.dtype is not _i8 or scales.dtype is not _f32 or index < 0 or \
+                scales.get_device() != index or not codes.is_contiguous() or \
+                not scales.is_contiguous():
+            _held("codes", index, codes, scales)
         shape = codes.shape
-        if K < 1 or len(shape) != 2 or shape[1] != _padded(K) or tuple(scales.shape) != shape[:1]:
+        if K < 1 or len(shape) != 2 or shape[1] != (K + 127) // 128 * 128 or \
+                scales.shape != shape[:1]:
             raise ValueError(f"codes [M, {_padded(K)}] and scales [M] are needed for K = {K}")
         self.codes, self.scales, self.M, self.K, self.index = codes, scales, shape[0], K, index
         c, s = codes.data_ptr(), scales.data_ptr()
@@ -93,21 +104,20 @@ class I8Tokens:
     @classmethod
     def empty(cls, M: int, K: int, device="cuda"):
         """Room for ``M`` tokens, uninitialised."""
-        return cls(torch.empty((M, _padded(K)), dtype=_i8, device=device),
-                   torch.empty(M, dtype=_f32, device=device), K)
+        return cls(torch.empty((M, (K + 127) // 128 * 128), dtype=_i8, device=device),
+                   torch.empty((M,), dtype=_f32, device=device), K)
 
 
-def _rows(t, name: str, dtype, shape, index: int):
-    """Checks a tensor of rows; returns its row distance."""
-    if t.dtype is not dtype or len(t.shape) != 2 or t.shape[1] != shape[1] or \
-            (shape[0] >= 0 and t.shape[0] != shape[0]) or t.get_device() != index or index < 0:
-        raise ValueError(f"{name}: [{'M' if shape[0] < 0 else shape[0]}, {shape[1]}] of {dtype} on "
-                         f"GPU {index} is needed, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+def _rows(t, name: str, dtype, M: int, K: int, index: int):
+    """Checks a tensor of rows [M, K]; returns its row distance."""
+    if t.dtype is not dtype or t.shape != (M, K) or t.get_device() != index or index < 0:
+        raise ValueError(f"{name}: [{M}, {K}] of {dtype} on GPU {index} is needed, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
     ld, one = t.stride()
-    if one != 1 and shape[1] != 1:
+    if one != 1 and K != 1:
         raise ValueError(f"{name}: unit stride along its columns is needed")
     # the stride of an axis of length one says nothing
-    return ld if t.shape[0] > 1 else shape[1]
+    return ld if M > 1 else K
 
 
 def _tokens(out, M: int, K: int, x) -> I8Tokens:
@@ -152,7 +162,7 @@ def quantize_tokens_i8(x, out=None) -> I8Tokens:
     dt = x.dtype
     _need(dt in _16BIT and x.dim() == 2 and x.shape[1] > 0, "x: [M, K] in bf16 or fp16 is needed")
     M, K = x.shape
-    ld = _rows(x, "x", dt, (M, K), x.get_device())
+    ld = _rows(x, "x", dt, M, K, x.get_device())
     out = _tokens(out, M, K, x)
     _call("qlora_quantize_tokens_i8", dt, out.index, x.data_ptr(), ld, M, K, out.codes.data_ptr(),
           out.scales.data_ptr())
@@ -180,17 +190,18 @@ def rms_norm_i8(x, weight, eps: float, residual=None, h=None, out=None):
     _need(dt in _16BIT and x.dim() == 2 and x.shape[1] > 0, "x: [M, K] in bf16 or fp16 is needed")
     M, K = x.shape
     index = x.get_device()
-    ldx = _rows(x, "x", dt, (M, K), index)
+    ldx = _rows(x, "x", dt, M, K, index)
     _dense(weight, "weight", dt, index)
-    _need(tuple(weight.shape) == (K,), f"weight: [{K}] is needed")
+    _need(weight.shape == (K,), f"weight: [{K}] is needed")
     rp = hp = None
     ldr = ldh = 0
     if residual is not None:
-        ldr = _rows(residual, "residual", dt, (M, K), index)
+        ldr = _rows(residual, "residual", dt, M, K, index)
         rp = residual.data_ptr()
         if h is None:
-            h = torch.empty((M, K), dtype=dt, device=x.device)
-        ldh = _rows(h, "h", dt, (M, K), index)
+            h, ldh = torch.empty((M, K), dtype=dt, device=x.device), K
+        else:
+            ldh = _rows(h, "h", dt, M, K, index)
         hp = h.data_ptr()
     else:
         _need(h is None, "h without residual")
@@ -205,31 +216,33 @@ def rms_norm_i8(x, weight, eps: float, residual=None, h=None, out=None):
 # products
 # ---------------------------------------------------------------------------
 
-def _product(name, ws, more, x, y, dtype):
-    """The call ``name`` of the weights ``ws`` and the arguments ``more``."""
-    w = ws[0]
-    N, index, M = w.N, w.index, x.M
-    if x.K != w.K or x.index != index:
-        raise ValueError(f"tokens of {w.K} values on GPU {index} are needed, got {x.K} on {x.device}")
-    args = [v.now() for v in ws]
-    tokens = x.now()
-    if dtype is None:
-        dtype = torch.bfloat16 if y is None else y.dtype
+def _place(w: I8Weight, x: I8Tokens, y, dtype):
+    """Checks the tokens and the output of a product; returns the output, its
+    type and its row distance."""
+    N, M = w.N, x.M
+    if x.K != w.K or x.index != w.index:
+        raise ValueError(f"tokens of {w.K} values on GPU {w.index} are needed, got {x.K} on "
+                         f"{x.device}")
+    if y is not None:
+        if dtype is None:
+            dtype = y.dtype
+        ld = _rows(y, "y", dtype, M, N, w.index)
+    elif dtype is None:
+        dtype = torch.bfloat16
     if dtype not in _16BIT:
         raise ValueError("bf16 or fp16 outputs")
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=x.device)
-        ldy = N
-    else:
-        ldy = _rows(y, "y", dtype, (M, N), index)
-    _call(name, dtype, index, *args, *more, tokens, y.data_ptr(), ldy)
-    return y
+        return torch.empty((M, N), dtype=dtype, device=x.device), dtype, N
+    return y, dtype, ld
 
 
 def linear_i8_fwd(iw: I8Weight, x: I8Tokens, y=None, dtype=None):
     """y = x . W^T of 8-bit tokens and an 8-bit weight, [M, N] in ``dtype``
     (bf16 or fp16; default: y's type, or bf16); y may have strided rows."""
-    return _product("qlora_linear_i8_fwd", (iw,), (), x, y, dtype)
+    w, t = iw.now(), x.now()
+    y, dtype, ld = _place(iw, x, y, dtype)
+    _call("qlora_linear_i8_fwd", dtype, iw.index, w, t, y.data_ptr(), ld)
+    return y
 
 
 def gated_i8_fwd(gate: I8Weight, up: I8Weight, x: I8Tokens, act: str = "silu", y=None, dtype=None):
@@ -241,4 +254,7 @@ def gated_i8_fwd(gate: I8Weight, up: I8Weight, x: I8Tokens, act: str = "silu", y
     if up.N != gate.N or up.K != gate.K or up.index != gate.index:
         raise ValueError(f"up: [{gate.N}, {gate.K}] on GPU {gate.index} is needed, got "
                          f"[{up.N}, {up.K}] on {up.device}")
-    return _product("qlora_gated_i8_fwd", (gate, up), (ACTS[act],), x, y, dtype)
+    g, u, t = gate.now(), up.now(), x.now()
+    y, dtype, ld = _place(gate, x, y, dtype)
+    _call("qlora_gated_i8_fwd", dtype, gate.index, g, u, ACTS[act], t, y.data_ptr(), ld)
+    return y

@@ -571,7 +571,7 @@ int qlora_kv4_attention_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch*
  * aligned (EALIGN).  No output may overlap an input or another output
  * (EINVAL) but where said so; of strided tensors that is the range from the
  * first to the last element, gaps included.  K is 1 .. 2^17 - 128, N
- * 1 .. 2^26 - 16, M 0 .. 2^30 (ESHAPE); M = 0 enqueues nothing.             */
+ * 1 .. 2^24 - 64, M 0 .. 2^30 (ESHAPE); M = 0 enqueues nothing.             */
 typedef struct qlora_i8_weight {
   const int8_t* tiles;   /* [ceil(N/16)][Kp/64][4][16][16] */
   const float*  scales;  /* [N]                            */
@@ -621,8 +621,8 @@ int qlora_rms_norm_i8_f16(const uint16_t* x, int64_t ldx, const uint16_t* residu
 /* y = x . W^T, [M, N] bf16 (_f16: fp16), rows ldy >= N elements apart; x->K
  * has to be w->K (EINVAL).  The sums of the codes' products are exact (int32);
  * y = sum * sw[n] * sx[m] in fp32, left to right, rounded once to 16 bits.
- * The same bits on every run and for every M.  M up to 2^20 - 16, and M * N
- * up to 2^34 (ESHAPE).  No workspace.                                        */
+ * The same bits on every run and for every M.  M up to 2^28, and M and N, each
+ * rounded up to 64, multiply to less than 2^34 (ESHAPE).  No workspace.      */
 int qlora_linear_i8_fwd(const qlora_i8_weight* w, const qlora_i8_tokens* x, uint16_t* y,
                         int64_t ldy, void* stream);
 int qlora_linear_i8_fwd_f16(const qlora_i8_weight* w, const qlora_i8_tokens* x, uint16_t* y,
