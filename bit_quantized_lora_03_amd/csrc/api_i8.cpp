@@ -16,8 +16,8 @@ namespace {
 // No sum of K products of two codes (-128 among them, which no quantiser
 // writes) passes 2^31.
 constexpr int64_t kMaxK = (int64_t{1} << 17) - qlora::kI8Pad;
-// A launch holds below 2^32 threads along x: the quantiser's 1024 for 4 rows.
-constexpr int64_t kMaxN = (int64_t{1} << 24) - 64;
+// A launch holds below 2^32 threads along x: the quantiser's 1024 for 2 rows.
+constexpr int64_t kMaxN = (int64_t{1} << 23) - 64;
 constexpr int64_t kMaxM = int64_t{1} << 30;
 // Tokens of a product: their scales have 32-bit offsets.
 constexpr int64_t kMaxLinearM = int64_t{1} << 28;

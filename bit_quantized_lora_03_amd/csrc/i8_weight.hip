@@ -1,12 +1,13 @@
 // A weight in the 8-bit row format and its tiles (i8_common.h): the quantiser
 // of fp32 rows and what they stand for.
 //
-// Bound by HBM: 4 bytes of a value in, one out.  A row of up to 16384 values
+// Bound by HBM: 4 bytes of a value in, one out.  A row of up to 32768 values
 // stays in registers between the search for its largest magnitude and its
-// codes: a block of sixteen waves has 16, 8 or 4 rows, by their length, and a
-// lane 64 values.  Longer rows are read twice, a wave a row.  Codes go through
-// LDS into the tiles' order, 16 KiB at a time, so stores are runs of a block's
-// rows (256, 128 or 64 bytes).
+// codes, 64 values a lane: one, two, four or eight waves have a row, and a block
+// eight waves (sixteen for the longest rows; with sixteen for all, one block a
+// CU, 11008 x 4096 took 55.6 us).  Longer rows are read twice, a wave a row.
+// Codes go through LDS into the tiles' order, 8 or 16 KiB at a time, so stores
+// are runs of a block's rows.
 
 #include "i8_common.h"
 #include "launch.h"
@@ -54,11 +55,7 @@ __global__ __launch_bounds__(1024) void quantize_i8_kernel(const float* __restri
     for (int i = 0; i < 4; ++i) {
       const int64_t k = k0 + 256 * i + 4 * lane;
       uint32_t c = 0;
-      if (row && k < K) {
-        const f32x4_t v = load4(src, k, K);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c |= ((uint32_t)i8_code(code, v[j]) & 0xFFu) << (8 * j);
-      }
+      if (row && k < K) c = i8_codes4(code, load4(src, k, K));
       *reinterpret_cast<uint32_t*>(&lds[wave * kLdsRow + 256 * i + 4 * lane]) = c;
     }
     __syncthreads();
@@ -70,17 +67,17 @@ __global__ __launch_bounds__(1024) void quantize_i8_kernel(const float* __restri
   }
 }
 
-// WR: waves of a row.
-template <int WR>
-__global__ __launch_bounds__(1024) void quantize_rows_i8_kernel(const float* __restrict__ w,
+// W: waves of the block, WR: of a row.
+template <int W, int WR>
+__global__ __launch_bounds__(64 * W) void quantize_rows_i8_kernel(const float* __restrict__ w,
                                                                 int N, int K,
                                                                 int8_t* __restrict__ tiles,
                                                                 float* __restrict__ scales) {
-  constexpr int R = 16 / WR;            // rows of the block
+  constexpr int R = W / WR;             // rows of the block
   constexpr int COLS = 1024 * WR;       // columns at a time
   constexpr int LD = COLS + 16;         // bytes of a row in LDS
   __shared__ __attribute__((aligned(16))) int8_t lds[2][R * LD];
-  __shared__ uint32_t tops[16];
+  __shared__ uint32_t tops[W];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = wave / WR, part = wave % WR;
   const int n = blockIdx.x * R + r, Kp = (int)i8_padded(K);
@@ -104,7 +101,7 @@ __global__ __launch_bounds__(1024) void quantize_rows_i8_kernel(const float* __r
   }
   const I8Row code = i8_row(__uint_as_float(top), 1.0, top < 0x7F800000u);
   if (row && lane == 0 && part == 0) scales[n] = code.s;
-  int8_t* dst = tiles + (int64_t)(blockIdx.x / WR) * 16 * Kp + (blockIdx.x % WR) * (16 * R);
+  int8_t* dst = tiles + (int64_t)(blockIdx.x / (16 / R)) * 16 * Kp + (blockIdx.x % (16 / R)) * (16 * R);
   // thread t stores 16 columns of row t % R
   const int t = threadIdx.x, tr = t % R, piece = t / R;
 #pragma unroll
@@ -113,10 +110,7 @@ __global__ __launch_bounds__(1024) void quantize_rows_i8_kernel(const float* __r
     int8_t* at = &lds[g & 1][r * LD + part * 256 + 4 * lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t c = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        c |= ((uint32_t)i8_code(code, v[4 * g + i][j]) & 0xFFu) << (8 * j);
+      const uint32_t c = i8_codes4(code, v[4 * g + i]);
       *reinterpret_cast<uint32_t*>(at + i * (256 * WR)) = row ? c : 0u;
     }
     __syncthreads();
@@ -127,31 +121,29 @@ __global__ __launch_bounds__(1024) void quantize_rows_i8_kernel(const float* __r
   }
 }
 
-// A wave has a row of the panel, a lane 16 columns of it: the sixteen waves
-// read the lines of a tile together.
+// A wave has a row of the panel, a lane 8 columns of it: the sixteen waves read
+// the lines of a tile together.
 template <class DT>
 __global__ __launch_bounds__(1024) void dequantize_i8_kernel(const int8_t* __restrict__ tiles,
                                                              const float* __restrict__ scales,
                                                              int64_t N, int64_t K,
                                                              uint16_t* __restrict__ out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 16 + wave, Kp = i8_padded(K);
+  const int64_t n = (int64_t)blockIdx.x * 16 + wave;
   if (n >= N) return;
   const float s = scales[n];
-  const int8_t* src = tiles + (int64_t)blockIdx.x * 16 * Kp + 16 * wave;
-  for (int64_t k = 16 * lane; k < K; k += kCols) {
-    const u32x4_t c =
-        *reinterpret_cast<const u32x4_t*>(src + (k >> 6) * kI8Tile + ((k >> 4) & 3) * 256);
+  const int8_t* src = tiles + (int64_t)blockIdx.x * 16 * i8_padded(K) + 16 * wave;
+  uint16_t* dst = out + n * K;
+  for (int k = 8 * lane; k < (int)K; k += 512) {
+    const u32x2_t c = *reinterpret_cast<const u32x2_t*>(src + (int64_t)(k >> 6) * kI8Tile +
+                                                        ((k >> 4) & 3) * 256 + (k & 8));
+    u32x4_t v;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      u32x4_t v;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t b = c[2 * q + j / 2] >> (16 * (j & 1));
-        v[j] = DT::pack2(i8_value((int8_t)b, s), i8_value((int8_t)(b >> 8), s));
-      }
-      if (k + 8 * q < K) store_piece(out + n * K, (int)k + 8 * q, (int)K, v);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t b = c[j / 2] >> (16 * (j & 1));
+      v[j] = DT::pack2(i8_value((int8_t)b, s), i8_value((int8_t)(b >> 8), s));
     }
+    store_piece(dst, k, (int)K, v);
   }
 }
 
@@ -161,11 +153,13 @@ hipError_t launch_quantize_i8(const float* w, int64_t N, int64_t K, int8_t* tile
                               hipStream_t s) {
   const unsigned panels = (unsigned)((N + 15) / 16);
   if (K <= 4096)
-    quantize_rows_i8_kernel<1><<<dim3(panels), 1024, 0, s>>>(w, (int)N, (int)K, tiles, scales);
+    quantize_rows_i8_kernel<8, 1><<<dim3(2 * panels), 512, 0, s>>>(w, (int)N, (int)K, tiles, scales);
   else if (K <= 8192)
-    quantize_rows_i8_kernel<2><<<dim3(2 * panels), 1024, 0, s>>>(w, (int)N, (int)K, tiles, scales);
+    quantize_rows_i8_kernel<8, 2><<<dim3(4 * panels), 512, 0, s>>>(w, (int)N, (int)K, tiles, scales);
   else if (K <= 16384)
-    quantize_rows_i8_kernel<4><<<dim3(4 * panels), 1024, 0, s>>>(w, (int)N, (int)K, tiles, scales);
+    quantize_rows_i8_kernel<8, 4><<<dim3(8 * panels), 512, 0, s>>>(w, (int)N, (int)K, tiles, scales);
+  else if (K <= 32768)
+    quantize_rows_i8_kernel<16, 8><<<dim3(8 * panels), 1024, 0, s>>>(w, (int)N, (int)K, tiles, scales);
   else
     quantize_i8_kernel<<<dim3(panels), 1024, 0, s>>>(w, N, K, tiles, scales);
   return hipGetLastError();

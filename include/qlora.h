@@ -571,7 +571,7 @@ int qlora_kv4_attention_f16(const qlora_kv4_cache* cache, const qlora_kv4_batch*
  * aligned (EALIGN).  No output may overlap an input or another output
  * (EINVAL) but where said so; of strided tensors that is the range from the
  * first to the last element, gaps included.  K is 1 .. 2^17 - 128, N
- * 1 .. 2^24 - 64, M 0 .. 2^30 (ESHAPE); M = 0 enqueues nothing.             */
+ * 1 .. 2^23 - 64, M 0 .. 2^30 (ESHAPE); M = 0 enqueues nothing.             */
 typedef struct qlora_i8_weight {
   const int8_t* tiles;   /* [ceil(N/16)][Kp/64][4][16][16] */
   const float*  scales;  /* [N]                            */

@@ -96,7 +96,7 @@ def scaled(sums, sw, sx):
 
 @pytest.mark.parametrize("N,K", [(1, 1), (1, 128), (3, 127), (16, 64), (17, 129), (40, 1000),
                                  (33, 1025), (100, 4097), (256, 2048), (19, 4096), (50, 8192),
-                                 (35, 8193), (21, 11008), (18, 16384), (17, 16385), (5, 40000)])
+                                 (35, 8193), (21, 11008), (18, 16384), (17, 16385), (3, 32768), (2, 32769), (5, 40000)])
 def test_quantize_weight(cuda, N, K):
     w = weights(N, K, N + K)
     w[0, :] = np.float32(0.25) * (np.arange(K) % 3 - 1)

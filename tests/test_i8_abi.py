@@ -16,7 +16,7 @@ MB = 1 << 20
 OK, EINVAL, ESHAPE, EALIGN, ENOTSUP = 0, -1, -2, -3, -4
 TAILS = pytest.mark.parametrize("tail", ["", "_f16"])
 SIZES = [((0, 64), EINVAL), ((-1, 64), EINVAL), ((16, 0), EINVAL), ((16, -64), EINVAL),
-         ((1 << 24, 64), ESHAPE), ((16, (1 << 17) - 127), ESHAPE), ((16, 1 << 40), ESHAPE)]
+         ((1 << 23, 64), ESHAPE), ((16, (1 << 17) - 127), ESHAPE), ((16, 1 << 40), ESHAPE)]
 
 
 def at(i):
@@ -160,7 +160,7 @@ def test_product_refusals(tail):
         assert h(t=tokens(M=1 << 27)) == ESHAPE            # 2^27 * 128
         for other in (at(0), at(1), at(2), at(3)):
             assert h(y=other) == EINVAL
-    assert f(w=weight(N=1 << 23, K=64), t=tokens(M=1 << 14, K=64), ldy=1 << 25) == ESHAPE
+    assert f(w=weight(N=1 << 22, K=64), t=tokens(M=1 << 15, K=64), ldy=1 << 25) == ESHAPE
     assert g(y=at(6)) == EINVAL and g(y=at(7)) == EINVAL
     assert g(act=2) == ENOTSUP and g(act=-1) == ENOTSUP
     assert g(up=weight(N=99)) == EINVAL and g(up=weight(K=301)) == EINVAL
