@@ -11,8 +11,8 @@
 // order, so a load is runs of 512 bytes) and never pass through LDS.  A tile
 // of K's operands are loaded two tiles ahead, into the registers that the tile
 // before last has left, step by step.  Tokens, which the waves share, reach LDS
-// by DMA, in a ring of four stages filled three tiles ahead, so one barrier a
-// tile is enough.  A stage's rows are 128 bytes, eight pieces; a piece lies at
+// by DMA, in a ring of four to eight stages filled as far ahead, so one barrier
+// a tile is enough.  A stage's rows are 128 bytes, eight pieces; a piece lies at
 // its number ^ (row / 2) % 8, so the 16 rows that a read serves in a cycle lie
 // in different banks.
 
@@ -31,13 +31,6 @@ constexpr int wait_imm(int vm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4)
 __device__ __forceinline__ i32x16_t mfma32(u32x4_t a, u32x4_t b, i32x16_t c) {
   return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a),
                                                __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
-}
-
-// act(g) u.  Both forms are g / (1 + exp(-z)): z = g, or for gelu's tanh form
-// z = 2 sqrt(2 / pi) (g + 0.044715 g^3).
-__device__ __forceinline__ float gated(float g, float u, int act) {
-  const float z = act == kI8Silu ? g : 1.5957691216057308f * fmaf(0.044715f * g * g, g, g);
-  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-z)) * u;
 }
 
 // The tile of a block.  Blocks go to the eight XCDs in turn; neighbouring ranks
@@ -102,7 +95,7 @@ struct Outputs {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             v[e] = i8_scaled(a[4 * q + e], sw[i][q][e], sx[j]);
-            if constexpr (G == 2) v[e] = gated(v[e], i8_scaled(b[4 * q + e], sw[1][q][e], sx[j]), p.act);
+            if constexpr (G == 2) v[e] = i8_gated(v[e], i8_scaled(b[4 * q + e], sw[1][q][e], sx[j]), p.act);
           }
           *reinterpret_cast<u32x2_t*>(lds + 16 * place(32 * j + lr, 4 * i + q) + 8 * lg) =
               u32x2_t{DT::pack2(v[0], v[1]), DT::pack2(v[2], v[3])};
@@ -130,28 +123,26 @@ struct Outputs {
   }
 };
 
-// KS: groups of four waves that each take a share of K.  WPE: waves of a SIMD
-// that the registers are to leave room for.
-template <class DT, int NI, int JT, int G, int KS, int WPE>
-__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(1, WPE)))
+template <class DT, int NI, int JT, int G>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2)))
 void gemm_i8_kernel(I8LinearArg p) {
   using S = Outputs<DT, NI, G, JT>;
   constexpr int TM = 32 * JT, RO = S::RO, TN = 4 * RO;
-  constexpr int ST = 4;                // stages of the tokens' ring
+  // Stages of the tokens' ring: more for the small tiles, whose work covers less
+  // of a load's way (32 x 128: 64 tokens, N and K 8192 take 19.0 us with four,
+  // 16.5 with eight; 64 x 128: 501 tokens, N and K 4096 13.3 with four, 12.7 with
+  // six; 128 x 128 loses with six).
+  constexpr int ST = JT == 1 ? 8 : JT == 2 ? 6 : 4;
   constexpr int WD = 2;                // tiles of K whose weights are held or on their way
   constexpr int XR = JT;               // DMA instructions of a wave a tile
   constexpr int LC = 4 * NI;           // loads of weights a tile
   constexpr int XST = TM * KT;         // bytes of a stage
   constexpr int SLOTS = NI * JT;       // matrix instructions a step
   constexpr int DP = 4 * SLOTS / XR;   // of these from one DMA to the next
-  constexpr int kSums = 4 * JT * NI * 4 * 64;  // of a share, in 16 bytes
-  constexpr int kRings = KS * ST * XST, kJoin = (KS - 1) * kSums * 16, kOut = 4 * S::kBytes;
-  constexpr int kLds = kRings > kJoin ? (kRings > kOut ? kRings : kOut) : (kJoin > kOut ? kJoin : kOut);
-  __shared__ __attribute__((aligned(16))) uint8_t lds_all[kLds];
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wave = wv % 4, share = wv / 4;
+  constexpr int kRing = ST * XST, kOut = 4 * S::kBytes;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing > kOut ? kRing : kOut];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 31, lg = lane >> 5;
-  uint8_t* const lds = lds_all + share * (ST * XST);
   const int64_t Kp = i8_padded(p.K), n_panels = (p.N + 15) / 16;
   uint32_t mt, nt;
   tile_of(blockIdx.x, gridDim.x, (uint32_t)((p.M + TM - 1) / TM), (uint32_t)((p.N + TN - 1) / TN),
@@ -164,9 +155,7 @@ void gemm_i8_kernel(I8LinearArg p) {
   constexpr int kSteady = (ST - 3) * (XR + LC) + NI, kFirst = (ST - 3) * XR + WD * LC;
   constexpr int kWait = kSteady < kFirst ? kSteady : kFirst;
   static_assert(kWait < 64 && ST >= 4, "outstanding operations of a wave");
-  // Every share has the same number of tiles, for they meet at barriers.
-  const int nkt = (int)(Kp / KT), each = (nkt + WD * KS - 1) / (WD * KS) * WD;
-  const int kt0 = each * share, kt1 = kt0 + each;
+  const int nkt = (int)(Kp / KT);
 
   // Operands of a weight: lane l has row l % 32 and 16 columns of a step of
   // 32.  Panels past the end read as zeros (the range check covers the lane's
@@ -230,13 +219,13 @@ void gemm_i8_kernel(I8LinearArg p) {
       __builtin_amdgcn_sched_barrier(0);
     };
     // x of the first two tiles, weights of the first, then the rest
-    dma_tile(kt0, 0);
-    dma_tile(kt0 + 1, 1);
-    load_tile(kt0, 0);
+    dma_tile(0, 0);
+    dma_tile(1, 1);
+    load_tile(0, 0);
 #pragma unroll
-    for (int d = 2; d < ST - 1; ++d) dma_tile(kt0 + d, d);
+    for (int d = 2; d < ST - 1; ++d) dma_tile(d, d);
 #pragma unroll
-    for (int d = 1; d < WD; ++d) load_tile(kt0 + d, d);
+    for (int d = 1; d < WD; ++d) load_tile(d, d);
     __builtin_amdgcn_s_waitcnt(wait_imm((ST - 3) * XR + WD * LC));
     __builtin_amdgcn_s_barrier();
 #pragma unroll
@@ -277,59 +266,22 @@ void gemm_i8_kernel(I8LinearArg p) {
       iteration(kt, phase, at(0), at(1), at(ST - 1));
       stage = stage + 1 < ST ? stage + 1 : 0;
     };
-    for (int kt = kt0; kt < kt1; kt += WD) {
+    for (int kt = 0; kt < nkt; kt += WD) {
       step(kt, std::integral_constant<int, 0>());
       step(kt + 1, std::integral_constant<int, 1>());
-      if constexpr (WD == 4) {
-        step(kt + 2, std::integral_constant<int, 2>());
-        step(kt + 3, std::integral_constant<int, 3>());
-      }
     }
     // what was asked for past the end is still on its way to LDS
     __builtin_amdgcn_s_waitcnt(wait_imm(0));
   }
   __syncthreads();
-  if constexpr (KS > 1) {
-    // the other shares' sums come to the first
-    i32x4_t* const sums = reinterpret_cast<i32x4_t*>(lds_all) + wave * (kSums / 4) + lane;
-    if (share > 0) {
-      i32x4_t* const mine = sums + (share - 1) * kSums;
-#pragma unroll
-      for (int j = 0; j < JT; ++j)
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mine[((j * NI + i) * 4 + q) * 64] = i32x4_t{acc[j][i][4 * q], acc[j][i][4 * q + 1],
-                                                        acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
-    }
-    __syncthreads();
-    if (share > 0) return;
-#pragma unroll
-    for (int k = 0; k < KS - 1; ++k)
-#pragma unroll
-      for (int j = 0; j < JT; ++j)
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const i32x4_t v = sums[k * kSums + ((j * NI + i) * 4 + q) * 64];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][i][4 * q + e] += v[e];
-          }
-    // a wave's outputs go where only its own sums were: no wait
-    static_assert(S::kBytes <= kSums / 4 * 16, "the wave's own place");
-    S::run(acc, p, n0 + wave * RO, m0, lds_all + wave * (kSums / 4 * 16), lane);
-  } else {
-    S::run(acc, p, n0 + wave * RO, m0, lds + wave * S::kBytes, lane);
-  }
+  S::run(acc, p, n0 + wave * RO, m0, lds + wave * S::kBytes, lane);
 }
 
-template <class DT, int NI, int JT, int G, int KS, int WPE>
+template <class DT, int NI, int JT, int G>
 void go(const I8LinearArg& p, hipStream_t s) {
   constexpr int TM = 32 * JT, TN = G == 2 ? 128 : 128 * NI;
   const int64_t blocks = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
-  gemm_i8_kernel<DT, NI, JT, G, KS, WPE><<<dim3((unsigned)blocks), 256 * KS, 0, s>>>(p);
+  gemm_i8_kernel<DT, NI, JT, G><<<dim3((unsigned)blocks), 256, 0, s>>>(p);
 }
 
 // Which tile.  What a tile of K (128 columns) takes, in us, as measured (gfx950,
@@ -368,21 +320,16 @@ template <class DT, int G>
 void pick(const I8LinearArg& p, hipStream_t s) {
   if constexpr (G == 2) {
     switch (best_of(kGated, p.M, p.N)) {
-      case 0: return go<DT, 2, 1, 2, 1, 2>(p, s);
-      case 1: return go<DT, 2, 2, 2, 1, 2>(p, s);
-      default: return go<DT, 2, 4, 2, 1, 2>(p, s);
+      case 0: return go<DT, 2, 1, 2>(p, s);
+      case 1: return go<DT, 2, 2, 2>(p, s);
+      default: return go<DT, 2, 4, 2>(p, s);
     }
   } else {
     switch (best_of(kPlain, p.M, p.N)) {
-      case 0:
-        // two shares of K where a CU has one block (64 tokens, N and K 8192:
-        // 19.1 us with one, 16.4 with two, 17.4 with four; 501 tokens, N 4096,
-        // two blocks a CU: 16.7, 16.9, 19.9)
-        if (((p.M + 31) / 32) * ((p.N + 127) / 128) <= 256) return go<DT, 1, 1, 1, 2, 4>(p, s);
-        return go<DT, 1, 1, 1, 1, 4>(p, s);
-      case 1: return go<DT, 1, 2, 1, 1, 4>(p, s);
-      case 2: return go<DT, 1, 4, 1, 1, 2>(p, s);
-      default: return go<DT, 2, 4, 1, 1, 2>(p, s);
+      case 0: return go<DT, 1, 1, 1>(p, s);
+      case 1: return go<DT, 1, 2, 1>(p, s);
+      case 2: return go<DT, 1, 4, 1>(p, s);
+      default: return go<DT, 2, 4, 1>(p, s);
     }
   }
 }

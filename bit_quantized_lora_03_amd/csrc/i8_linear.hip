@@ -24,13 +24,6 @@ __device__ __forceinline__ i32x4_t mfma16(u32x4_t a, u32x4_t b, i32x4_t c) {
                                                __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
 }
 
-// act(g) u.  Both forms are g / (1 + exp(-z)): z = g, or for gelu's tanh form
-// z = 2 sqrt(2 / pi) (g + 0.044715 g^3).
-__device__ __forceinline__ float gated(float g, float u, int act) {
-  const float z = act == kI8Silu ? g : 1.5957691216057308f * fmaf(0.044715f * g * g, g, g);
-  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-z)) * u;
-}
-
 // Four neighbouring outputs of a token, n .. n + 3 of which N has some.
 template <class DT>
 __device__ __forceinline__ void store4(uint16_t* row, int64_t n, int64_t N, bool whole,
@@ -129,7 +122,7 @@ __global__ __launch_bounds__(64 * W) void few_i8_kernel(I8LinearArg p) {
     for (int j = 0; j < 4; ++j) {
       const int64_t row = n + j < p.N ? n + j : p.N - 1;
       v[j] = i8_scaled(sum[0][j], p.wscale[0][row], sx);
-      if constexpr (G == 2) v[j] = gated(v[j], i8_scaled(sum[1][j], p.wscale[1][row], sx), p.act);
+      if constexpr (G == 2) v[j] = i8_gated(v[j], i8_scaled(sum[1][j], p.wscale[1][row], sx), p.act);
     }
     store4<DT>(p.y + m * p.ldy, n, p.N, vec && n + 4 <= p.N, v);
   }

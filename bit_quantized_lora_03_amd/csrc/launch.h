@@ -282,9 +282,8 @@ struct I8LinearArg {
   const float* xscale;
   uint16_t* y;
   int64_t ldy, M, N, K;
-  int act;  // kI8Silu, kI8Gelu
+  int act;  // kI8Silu or kI8Gelu (i8_common.h)
 };
-constexpr int kI8Silu = 0, kI8Gelu = 1;
 hipError_t launch_linear_i8(const I8LinearArg& p, bool f16, hipStream_t s);
 // i8_gemm.hip -- its form for many tokens
 hipError_t launch_gemm_i8(const I8LinearArg& p, bool f16, hipStream_t s);

@@ -104,8 +104,14 @@ class I8Tokens:
     @classmethod
     def empty(cls, M: int, K: int, device="cuda"):
         """Room for ``M`` tokens, uninitialised."""
-        return cls(torch.empty((M, (K + 127) // 128 * 128), dtype=_i8, device=device),
-                   torch.empty((M,), dtype=_f32, device=device), K)
+        codes = torch.empty((M, (K + 127) // 128 * 128), dtype=_i8, device=device)
+        scales = torch.empty((M,), dtype=_f32, device=device)
+        t = cls.__new__(cls)
+        t.codes, t.scales, t.M, t.K, t.index = codes, scales, M, K, codes.get_device()
+        c, s = codes.data_ptr(), scales.data_ptr()
+        t.at = codes, c, scales, s
+        t.struct = I8TokensStruct(c, s, M, K)
+        return t
 
 
 def _rows(t, name: str, dtype, M: int, K: int, index: int):
@@ -123,9 +129,9 @@ def _rows(t, name: str, dtype, M: int, K: int, index: int):
 def _tokens(out, M: int, K: int, x) -> I8Tokens:
     if out is None:
         return I8Tokens.empty(M, K, x.device)
-    _need(out.M == M and out.K == K and out.index == x.get_device(),
-          f"out: tokens [{M}, {K}] on {x.device} are needed")
     out.now()
+    if out.M != M or out.K != K or out.index != x.get_device():
+        raise ValueError(f"out: tokens [{M}, {K}] on {x.device} are needed")
     return out
 
 
@@ -160,8 +166,10 @@ def quantize_tokens_i8(x, out=None) -> I8Tokens:
     """x [M, K] bf16 or fp16 (rows may be strided) -> I8Tokens, one scale per
     token, into ``out`` where it is given."""
     dt = x.dtype
-    _need(dt in _16BIT and x.dim() == 2 and x.shape[1] > 0, "x: [M, K] in bf16 or fp16 is needed")
-    M, K = x.shape
+    shape = x.shape
+    if dt not in _16BIT or len(shape) != 2 or shape[1] == 0:
+        raise ValueError("x: [M, K] in bf16 or fp16 is needed")
+    M, K = shape
     ld = _rows(x, "x", dt, M, K, x.get_device())
     out = _tokens(out, M, K, x)
     _call("qlora_quantize_tokens_i8", dt, out.index, x.data_ptr(), ld, M, K, out.codes.data_ptr(),
@@ -187,12 +195,15 @@ def rms_norm_i8(x, weight, eps: float, residual=None, h=None, out=None):
     The sum goes into ``h`` where it is given, which may be x or residual, and
     the tokens into ``out``."""
     dt = x.dtype
-    _need(dt in _16BIT and x.dim() == 2 and x.shape[1] > 0, "x: [M, K] in bf16 or fp16 is needed")
-    M, K = x.shape
+    shape = x.shape
+    if dt not in _16BIT or len(shape) != 2 or shape[1] == 0:
+        raise ValueError("x: [M, K] in bf16 or fp16 is needed")
+    M, K = shape
     index = x.get_device()
     ldx = _rows(x, "x", dt, M, K, index)
     _dense(weight, "weight", dt, index)
-    _need(weight.shape == (K,), f"weight: [{K}] is needed")
+    if weight.shape != (K,):
+        raise ValueError(f"weight: [{K}] is needed")
     rp = hp = None
     ldr = ldh = 0
     if residual is not None:
