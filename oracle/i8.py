@@ -62,8 +62,9 @@ def tile(c):
 
 
 def sums(cx, cw):
-    """Exact integer sums [M, N] of the codes' products."""
-    return np.asarray(cx, dtype=np.int64) @ np.asarray(cw, dtype=np.int64).T
+    """Exact integer sums [M, N] of the codes' products (below 2^53 in fp64
+    whatever the order)."""
+    return (np.asarray(cx, dtype=np.float64) @ np.asarray(cw, dtype=np.float64).T).astype(np.int64)
 
 
 def product(cx, sx, cw, sw):

@@ -328,6 +328,24 @@ def test_product(cuda, M, N, K, dtype):
     assert torch.equal(q.linear_i8_fwd(iw, t, dtype=tdtype(dtype)), y.t)
 
 
+# each of the tiles, at its edges: 32 x 128, 64 x 128, 128 x 128, 128 x 256,
+# with K of one tile and of even and odd numbers of them
+WIDE = [(33, 4000, 100), (97, 11000, 130), (130, 8192, 257), (200, 11008, 300), (230, 10900, 384),
+        (500, 4096, 513), (501, 4091, 128), (700, 8192, 200), (1025, 8200, 256), (2047, 5001, 640),
+        (3000, 2053, 1111)]
+
+
+@TYPES
+@pytest.mark.parametrize("M,N,K", WIDE)
+def test_product_of_every_tile(cuda, M, N, K, dtype):
+    iw, cw, sw = i8_weight(weights(N, K, M))
+    t, cx, sx = i8_tokens(M, K, N)
+    y = Guarded((M, N), tdtype(dtype))
+    q.linear_i8_fwd(iw, t, y=y.t)
+    y.check("y")
+    assert np.array_equal(bits(y.t), round16(scaled(i8.sums(cx, cw), sw, sx), dtype))
+
+
 @pytest.mark.parametrize("M", [1, 3, 20, 64, 100, 300])
 @pytest.mark.parametrize("K", [1 << 12, (1 << 17) - 128])
 def test_largest_sums(cuda, M, K):
@@ -397,7 +415,10 @@ def gated_ref(cx, sx, cg, sg, cu, su, act):
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 100, 300), (4, 1000, 128), (16, 35, 2000),
                                    (30, 64, 640), (64, 200, 1000), (65, 130, 512), (128, 128, 256),
-                                   (200, 300, 1500), (300, 513, 1024), (520, 260, 700)])
+                                   (200, 300, 1500), (300, 513, 1024), (520, 260, 700),
+                                   # each of the tiles: 32, 64 and 128 tokens
+                                   (33, 5000, 300), (100, 11008, 140), (301, 11000, 130),
+                                   (1030, 4096, 257)])
 def test_gated(cuda, M, N, K, act, dtype):
     rng = np.random.default_rng(M)
     gate, cg, sg = i8_weight(weights(N, K, 1) * rng.choice([0.1, 1, 10], (N, 1)).astype(np.float32))
@@ -622,6 +643,79 @@ def test_captured_and_replayed(cuda, M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(h, wh)
+
+
+class Layer(Block):
+    """A served layer: the block above behind attention over a 4-bit paged
+    cache, whose queries, keys and values are slices of one product."""
+
+    def __init__(self, hidden, ffn, heads, kv_heads, D, dtype):
+        import torch
+        super().__init__(hidden, ffn, dtype)
+        self.heads, self.kv, self.D = heads, kv_heads, D
+        self.w0 = (1 + 0.1 * torch.randn(hidden, device="cuda")).to(self.dt)
+        self.qkv = q.quantize_i8(torch.randn((heads + 2 * kv_heads) * D, hidden, device="cuda") * 0.05)
+        self.o = q.quantize_i8(torch.randn(hidden, heads * D, device="cuda") * 0.05)
+        a = torch.arange(256, device="cuda")[:, None] * 10000.0 ** (-torch.arange(0, D, 2, device="cuda") / D)
+        self.angles = torch.cat([a.cos(), a.sin()], -1).float()
+
+    def attend(self, x, cache, cu, lens, table, max_q):
+        t, h = q.rms_norm_i8(x, self.w0, 1e-5)
+        p = q.linear_i8_fwd(self.qkv, t, dtype=self.dt).unflatten(1, (-1, self.D))
+        r = q.kv4_append(cache, p[:, self.heads:self.heads + self.kv], p[:, self.heads + self.kv:],
+                         cu, lens, table, max_q, q=p[:, :self.heads], cos_sin=self.angles)
+        a = q.kv4_attention(cache, r, cu, lens, table, max_q, 256)
+        return q.linear_i8_fwd(self.o, q.quantize_tokens_i8(a.flatten(1)), dtype=self.dt), h
+
+
+@TYPES
+def test_a_layer_prompt_then_captured_decode(cuda, dtype):
+    """Three prompts, then single tokens through a captured step that is
+    replayed for other tokens and lengths: the eager step's bits."""
+    import torch
+    torch.manual_seed(0)
+    B, hidden, page = 3, 384, 16
+    layer = Layer(hidden, 700, 8, 2, 64, dtype)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    new = [37, 5, 60]
+    table = torch.randperm(B * 16, device="cuda").to(torch.int32).view(B, 16)
+
+    def caches():
+        c = q.Kv4Cache.empty(B * 16, page, 2, 64)
+        for n in ("k_codes", "k_pairs", "v_codes", "v_pairs"):
+            getattr(c, n).zero_()
+        return c
+
+    def prompt(cache):
+        x = torch.randn(sum(new), hidden, generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(layer.dt)
+        a, h = layer.attend(x, cache, ints([0, 37, 42, 102]), ints(new), table, 60)
+        return layer(a, h.clone())[0]
+
+    eager, graphed = caches(), caches()
+    y = prompt(eager)
+    assert torch.isfinite(y).all() and torch.equal(y, prompt(graphed))
+    cu, lens = ints([0, 1, 2, 3]), ints(new)
+    x = torch.zeros(B, hidden, dtype=layer.dt, device="cuda")
+    step = lambda c, x, n: layer(*layer.attend(x, c, cu, n, table, 1))  # noqa: E731
+    spare = caches()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(spare, x.clone(), lens)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = step(graphed, x, lens)
+    for i in range(4):
+        now = ints([n + 1 + i for n in new])
+        token = torch.randn(B, hidden, device="cuda").to(layer.dt)
+        want, _ = step(eager, token.clone(), now)
+        x.copy_(token)
+        lens.copy_(now)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.isfinite(want).all() and torch.equal(out, want)
+    assert torch.equal(eager.k_codes, graphed.k_codes) and torch.equal(eager.v_codes, graphed.v_codes)
 
 
 def test_same_bits_on_every_run(cuda):
