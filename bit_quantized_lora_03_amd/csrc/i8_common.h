@@ -52,28 +52,6 @@ __device__ __forceinline__ int i8_code(const I8Row& w, double v) {
   return w.ok ? (int)__builtin_rint(q) : 0;
 }
 
-// Four codes of fp32 values, packed.  v (127 / a) in fp32 is off by less than
-// 127 2^-23, so it decides all but the values next to a border; only for these
-// (one in 2^14) the exact quotients are worked out.  That takes 3 to 10 % less
-// time than fp64 for all.
-__device__ __forceinline__ uint32_t i8_codes4(const I8Row& w, f32x4_t v) {
-  const float a = (float)w.a, r = 127.0f / a;
-  bool sure = a > 1e-30f && a < 1e30f;
-  uint32_t c = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float t = v[j] * r, n = __builtin_rintf(t);
-    sure = sure && fabsf(t - n) < 0.5f - 0x1p-15f;
-    c |= ((uint32_t)(int)n & 0xFFu) << (8 * j);
-  }
-  if (!sure) {
-    c = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c |= ((uint32_t)i8_code(w, v[j]) & 0xFFu) << (8 * j);
-  }
-  return w.ok ? c : 0u;
-}
-
 // What a code stands for, and a sum of products of codes: each product is
 // rounded to fp32.  (The compiler makes one instruction with one rounding of
 // the last and a conversion to fp16 where it sees both, also with contraction

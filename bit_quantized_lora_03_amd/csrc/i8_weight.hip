@@ -55,7 +55,11 @@ __global__ __launch_bounds__(1024) void quantize_i8_kernel(const float* __restri
     for (int i = 0; i < 4; ++i) {
       const int64_t k = k0 + 256 * i + 4 * lane;
       uint32_t c = 0;
-      if (row && k < K) c = i8_codes4(code, load4(src, k, K));
+      if (row && k < K) {
+        const f32x4_t v = load4(src, k, K);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c |= ((uint32_t)i8_code(code, v[j]) & 0xFFu) << (8 * j);
+      }
       *reinterpret_cast<uint32_t*>(&lds[wave * kLdsRow + 256 * i + 4 * lane]) = c;
     }
     __syncthreads();
@@ -110,7 +114,10 @@ __global__ __launch_bounds__(64 * W) void quantize_rows_i8_kernel(const float* _
     int8_t* at = &lds[g & 1][r * LD + part * 256 + 4 * lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t c = i8_codes4(code, v[4 * g + i]);
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        c |= ((uint32_t)i8_code(code, v[4 * g + i][j]) & 0xFFu) << (8 * j);
       *reinterpret_cast<uint32_t*>(at + i * (256 * WR)) = row ? c : 0u;
     }
     __syncthreads();
