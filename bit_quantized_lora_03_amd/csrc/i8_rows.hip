@@ -12,6 +12,10 @@
 // barrier), up to 16384 to four, longer ones to sixteen.  Sums, maxima and
 // quotients are fp64: with a product of two 16-bit floats exact in it nothing
 // overflows, and its share is small beside the memory's.
+//
+// Measured: 4096 tokens of 8192 20 us, with the norm and a residual 47 (5.0 TB/s;
+// a large copy 5.16); 2047 of 11008 16.1 and 41; one of 4096 2.5 and 3.9 in a
+// replayed graph.
 
 #include <type_traits>
 

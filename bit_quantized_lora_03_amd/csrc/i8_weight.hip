@@ -8,6 +8,9 @@
 // CU, 11008 x 4096 took 55.6 us).  Longer rows are read twice, a wave a row.
 // Codes go through LDS into the tiles' order, 8 or 16 KiB at a time, so stores
 // are runs of a block's rows.
+//
+// Measured: 11008 x 4096 42 us, 22016 x 8192 181 (902 MB, 5.0 TB/s; a large copy
+// 5.16), 4096 x 11008 54, 8192 x 28672 355; reading the first two back 22 and 117.
 
 #include "i8_common.h"
 #include "launch.h"

@@ -104,6 +104,8 @@ class I8Tokens:
     @classmethod
     def empty(cls, M: int, K: int, device="cuda"):
         """Room for ``M`` tokens, uninitialised."""
+        if K < 1:
+            raise ValueError(f"K = {K}: tokens have at least one value")
         codes = torch.empty((M, (K + 127) // 128 * 128), dtype=_i8, device=device)
         scales = torch.empty((M,), dtype=_f32, device=device)
         t = cls.__new__(cls)

@@ -330,7 +330,7 @@ def test_product(cuda, M, N, K, dtype):
 
 # each of the tiles, at its edges: 32 x 128, 64 x 128, 128 x 128, 128 x 256,
 # with K of one tile and of even and odd numbers of them
-WIDE = [(33, 4000, 100), (97, 11000, 130), (130, 8192, 257), (200, 11008, 300), (230, 10900, 384),
+WIDE = [(17, 4096, 128), (20, 5000, 300), (32, 4097, 200), (33, 4000, 100), (97, 11000, 130), (130, 8192, 257), (200, 11008, 300), (230, 10900, 384),
         (500, 4096, 513), (501, 4091, 128), (700, 8192, 200), (1025, 8200, 256), (2047, 5001, 640),
         (3000, 2053, 1111)]
 
@@ -374,6 +374,28 @@ def test_product_into_strided_rows(cuda, M, N, K, left, right, dtype):
     assert q.linear_i8_fwd(iw, t, y=y) is y
     assert np.array_equal(bits(y), round16(scaled(i8.sums(cx, cw), sw, sx), dtype))
     assert (wide[:, :left] == 7).all() and (wide[:, left + N:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [5, 60, 300])
+def test_codes_at_any_multiple_of_16_bytes(cuda, M):
+    import torch
+    N, K = 200, 900
+    iw, cw, sw = i8_weight(weights(N, K, 4))
+    t, cx, sx = i8_tokens(M, K, 5)
+
+    def moved(a):
+        b = torch.empty(a.numel() + 16, dtype=torch.int8, device="cuda")[16:].view(a.shape)
+        return b.copy_(a)
+
+    s = torch.empty(N + 1, device="cuda")[1:].copy_(iw.scales)
+    y = q.linear_i8_fwd(q.I8Weight(moved(iw.tiles), s, N, K), q.I8Tokens(moved(t.codes), t.scales, K))
+    assert np.array_equal(bits(y), round16(scaled(i8.sums(cx, cw), sw, sx), "bf16"))
+    # and tokens written there
+    x, v = activations(M, K, "bf16", 6)
+    out = q.I8Tokens(moved(t.codes), torch.empty(M + 1, device="cuda")[1:], K)
+    q.quantize_tokens_i8(x, out=out)
+    c, s = i8.encode(v)
+    assert np.array_equal(out.codes.cpu().numpy(), i8.pad(c)) and np.array_equal(out.scales.cpu().numpy(), s)
 
 
 def test_nan_scales_reach_their_rows_and_columns_only(cuda):

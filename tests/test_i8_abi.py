@@ -183,7 +183,8 @@ def test_python_refuses_cpu_tensors_and_types():
                                     torch.zeros(4, dtype=torch.bfloat16), 1e-5),
               lambda: q.rms_norm_i8(torch.zeros(4, 4), torch.zeros(4), 1e-5),
               lambda: q.I8Weight(torch.zeros(1, 2, 4, 16, 16, dtype=torch.int8), torch.zeros(4), 4, 4),
-              lambda: q.I8Tokens(torch.zeros(4, 128, dtype=torch.int8), torch.zeros(4), 4)):
+              lambda: q.I8Tokens(torch.zeros(4, 128, dtype=torch.int8), torch.zeros(4), 4),
+              lambda: q.I8Tokens.empty(4, 0, device="cpu")):
         with pytest.raises(ValueError):
             f()
 
