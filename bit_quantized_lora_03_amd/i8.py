@@ -108,8 +108,11 @@ class I8Tokens:
             raise ValueError(f"K = {K}: tokens have at least one value")
         codes = torch.empty((M, (K + 127) // 128 * 128), dtype=_i8, device=device)
         scales = torch.empty((M,), dtype=_f32, device=device)
+        index = codes.get_device()
+        if index < 0:
+            raise ValueError(f"tokens on the GPU are needed, not on {codes.device}")
         t = cls.__new__(cls)
-        t.codes, t.scales, t.M, t.K, t.index = codes, scales, M, K, codes.get_device()
+        t.codes, t.scales, t.M, t.K, t.index = codes, scales, M, K, index
         c, s = codes.data_ptr(), scales.data_ptr()
         t.at = codes, c, scales, s
         t.struct = I8TokensStruct(c, s, M, K)

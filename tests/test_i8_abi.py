@@ -189,6 +189,13 @@ def test_python_refuses_cpu_tensors_and_types():
             f()
 
 
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_room_for_tokens_is_on_the_gpu(device):
+    """Tokens of host memory would be given to a kernel."""
+    with pytest.raises(ValueError, match="GPU"):
+        q.I8Tokens.empty(4, 64, device=device)
+
+
 def test_merge_takes_i8_by_name():
     with pytest.raises(ValueError, match="fp32 merge"):
         q.merge_adapter(torch.zeros(4, 4), None, None, 1.0, out_f32=False, requantize="i8")
