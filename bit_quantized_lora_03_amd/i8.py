@@ -58,8 +58,9 @@ class I8Weight:
         """The descriptor of the tensors as they are: checked and written anew
         where one was exchanged or has other memory since."""
         tiles, t, scales, s = self.at
+        struct = self.struct
         if self.tiles is not tiles or self.scales is not scales or tiles.data_ptr() != t or \
-                scales.data_ptr() != s:
+                scales.data_ptr() != s or self.N != struct.N or self.K != struct.K:
             self.__init__(self.tiles, self.scales, self.N, self.K)
         return self.struct
 
@@ -92,8 +93,9 @@ class I8Tokens:
     def now(self) -> I8TokensStruct:
         """The descriptor of the tensors as they are (as :meth:`I8Weight.now`)."""
         codes, c, scales, s = self.at
+        struct = self.struct
         if self.codes is not codes or self.scales is not scales or codes.data_ptr() != c or \
-                scales.data_ptr() != s:
+                scales.data_ptr() != s or self.M != struct.M or self.K != struct.K:
             self.__init__(self.codes, self.scales, self.K)
         return self.struct
 
@@ -267,10 +269,10 @@ def gated_i8_fwd(gate: I8Weight, up: I8Weight, x: I8Tokens, act: str = "silu", y
     :func:`linear_i8_fwd`."""
     if act not in ACTS:
         raise ValueError(f"act: one of {tuple(ACTS)} is needed, not {act!r}")
+    g, u, t = gate.now(), up.now(), x.now()
     if up.N != gate.N or up.K != gate.K or up.index != gate.index:
         raise ValueError(f"up: [{gate.N}, {gate.K}] on GPU {gate.index} is needed, got "
                          f"[{up.N}, {up.K}] on {up.device}")
-    g, u, t = gate.now(), up.now(), x.now()
     y, dtype, ld = _place(gate, x, y, dtype)
     _call("qlora_gated_i8_fwd", dtype, gate.index, g, u, ACTS[act], t, y.data_ptr(), ld)
     return y

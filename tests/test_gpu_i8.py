@@ -545,6 +545,25 @@ def test_handles_follow_their_tensors(cuda):
         q.linear_i8_fwd(iw, t)
 
 
+def test_handles_keep_their_sizes(cuda):
+    """A size that is assigned is the tensors' or refused: outputs are made by
+    it and written by the tensors' sizes."""
+    iw, _, _ = i8_weight(weights(33, 300, 1))
+    t, _, _ = i8_tokens(4, 300, 2)
+    t.M = 2
+    assert q.linear_i8_fwd(iw, t).shape == (4, 33)
+    t.M = 9
+    assert q.dequantize_tokens_i8(t).shape == (4, 300)
+    for h, name, value in ((t, "K", 512), (iw, "N", 7), (iw, "K", 128)):
+        was = getattr(h, name)
+        setattr(h, name, value)
+        for f in (lambda: q.linear_i8_fwd(iw, t), lambda: q.gated_i8_fwd(iw, iw, t)):
+            with pytest.raises(ValueError):
+                f()
+        setattr(h, name, was)
+    assert q.linear_i8_fwd(iw, t).shape == (4, 33)
+
+
 def test_merge_to_8_bits(cuda):
     import torch
     w = dev(weights(128, 256, 3))
