@@ -52,10 +52,11 @@ __device__ __forceinline__ int i8_code(const I8Row& w, double v) {
   return w.ok ? (int)__builtin_rint(q) : 0;
 }
 
-// What a code stands for, and a sum of products of codes: each product is
-// rounded to fp32.  (The compiler makes one instruction with one rounding of
-// the last and a conversion to fp16 where it sees both, also with contraction
-// off, so it is not let to.)
+// What a code stands for, a sum of products of codes, and a gated value: each
+// product is rounded to fp32.  (The compiler makes one instruction with one
+// rounding of the last and a conversion to fp16 where it sees both, also with
+// contraction off, so it is not let to: a gated value in fp16 depended on the
+// kernel, so on the number of tokens.)
 __device__ __forceinline__ float i8_value(int8_t c, float s) {
   float v = (float)c * s;
   asm("" : "+v"(v));
@@ -72,7 +73,9 @@ constexpr int kI8Silu = 0, kI8Gelu = 1;
 // z = 2 sqrt(2 / pi) (g + 0.044715 g^3).
 __device__ __forceinline__ float i8_gated(float g, float u, int act) {
   const float z = act == kI8Silu ? g : 1.5957691216057308f * fmaf(0.044715f * g * g, g, g);
-  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-z)) * u;
+  float v = g * __builtin_amdgcn_rcpf(1.0f + __expf(-z)) * u;
+  asm("" : "+v"(v));
+  return v;
 }
 
 // Eight neighbouring 16-bit floats of a row that ends at K; rows may start at

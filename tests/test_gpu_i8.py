@@ -376,6 +376,47 @@ def test_product_into_strided_rows(cuda, M, N, K, left, right, dtype):
     assert (wide[:, :left] == 7).all() and (wide[:, left + N:] == 7).all()
 
 
+# sizes of which each form and tile has some: 16 x 16, 32 x 16, 32 x 32, 64 x 32,
+# 32 x 128, 64 x 128, 128 x 128, 128 x 256
+FORMS = [(57, 105, 399), (21, 3545, 403), (322, 451, 67), (38, 5106, 1496), (35, 7888, 389),
+         (167, 7097, 66), (203, 7630, 514), (993, 7112, 396)]
+
+
+@TYPES
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_every_form(cuda, M, N, K, dtype):
+    """Strided outputs, handles at any multiple of 16 bytes, NaN scales and
+    rows of padding, in each of the forms."""
+    import torch
+    iw, cw, sw = i8_weight(weights(N, K, M))
+    t, cx, sx = i8_tokens(M, K, N)
+    sw, sx = sw.copy(), sx.copy()
+    sw[N // 3] = sx[M - 1] = np.nan
+
+    def moved(a):
+        b = torch.empty(a.numel() + 16, dtype=torch.int8, device="cuda")[16:].view(a.shape)
+        return b.copy_(a)
+
+    tiles = moved(iw.tiles)
+    if N % 16:
+        tiles[-1, :, :, N % 16:] = 101
+    w = q.I8Weight(tiles, dev(sw), N, K)
+    x = q.I8Tokens(moved(t.codes), dev(sx), K)
+    with np.errstate(invalid="ignore"):
+        want = torch.from_numpy(round16(scaled(i8.sums(cx, cw), sw, sx), dtype).view(np.int16))
+    want = want.view(tdtype(dtype))
+    for left, right in ((0, 0), (1, 2), (8, 8), (4, N % 2)):
+        big = torch.full((M, left + N + right), 7, dtype=tdtype(dtype), device="cuda")
+        y = big[:, left:left + N]
+        q.linear_i8_fwd(w, x, y=y)
+        y = y.cpu()
+        nan = torch.isnan(y)
+        assert nan[:, N // 3].all() and nan[M - 1].all()
+        assert int(nan.sum()) == M + N - 1
+        assert torch.equal(y[~nan], want[~nan])
+        assert (big[:, :left] == 7).all() and (big[:, left + N:] == 7).all()
+
+
 @pytest.mark.parametrize("M", [5, 60, 300])
 def test_codes_at_any_multiple_of_16_bytes(cuda, M):
     import torch
@@ -455,6 +496,25 @@ def test_gated(cuda, M, N, K, act, dtype):
     # the two are not exchanged
     other, _ = gated_ref(cx, sx, cu, su, cg, sg, act)
     assert M * N * K == 1 or not np.all(np.abs(f64(y.t) - other) <= 0.1 * np.abs(other) + 1e-3)
+
+
+@TYPES
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,N,K", [(57, 105, 399), (55, 5542, 67), (21, 7229, 288), (38, 4199, 1703),
+                                   (97, 7393, 79), (170, 7278, 129), (226, 8773, 668)])
+def test_gated_in_every_form(cuda, M, N, K, act, dtype):
+    gate, cg, sg = i8_weight(weights(N, K, 1))
+    up, cu, su = i8_weight(weights(N, K, 2))
+    t, cx, sx = i8_tokens(M, K, 3)
+    import torch
+    big = torch.full((M, N + 3), 7, dtype=tdtype(dtype), device="cuda")
+    y = q.gated_i8_fwd(gate, up, t, act=act, y=big[:, 1:N + 1])
+    ref, bar = gated_ref(cx, sx, cg, sg, cu, su, act)
+    assert np.all(np.abs(f64(y) - ref) <= U16[dtype] * (np.abs(ref) + bar) + bar + 2.0 ** -25)
+    assert (big[:, :1] == 7).all() and (big[:, N + 1:] == 7).all()
+    # a token alone gives the same bits, in whichever form
+    one = q.I8Tokens(t.codes[M // 2:M // 2 + 1], t.scales[M // 2:M // 2 + 1], K)
+    assert torch.equal(q.gated_i8_fwd(gate, up, one, act=act, dtype=tdtype(dtype))[0], y[M // 2])
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
