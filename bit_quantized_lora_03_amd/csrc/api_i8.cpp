@@ -175,7 +175,8 @@ int linear(const qlora_i8_weight* w, const qlora_i8_weight* up, bool gated, int3
     if (x->K != w->K) return QLORA_EINVAL;
     if (x->M == 0) return QLORA_OK;
     if (!y || ldy < w->N) return QLORA_EINVAL;
-    // a grid has at most two blocks, of 256 threads, for each 64 x 64 outputs
+    // a grid of large tiles has at most two blocks, of 256 threads, for each 64 x 64
+    // outputs, one of small tiles is taken below 2^22 blocks of 512
     if (ldy > kMaxStride || x->M > kMaxLinearM ||
         ((x->M + 63) / 64) * ((w->N + 63) / 64) >= (int64_t{1} << 22))
       return QLORA_ESHAPE;

@@ -78,6 +78,20 @@ __device__ __forceinline__ float i8_gated(float g, float u, int act) {
   return v;
 }
 
+// The tile of a block.  Blocks go to the eight XCDs in turn; neighbouring ranks
+// are made to be on one, whose L2 then holds what they share.  Ranks walk bands
+// of 1024 tokens, a column of tiles of the band at a time.
+__device__ __forceinline__ void i8_tile_of(uint32_t id, uint32_t total, uint32_t m_tiles,
+                                           uint32_t n_tiles, uint32_t band, uint32_t& m,
+                                           uint32_t& n) {
+  const uint32_t xcd = id % 8, per = total / 8, extra = total % 8;
+  const uint32_t rank = xcd * per + min(xcd, extra) + id / 8;
+  const uint32_t span = band * n_tiles, g = rank / span, w = rank - g * span;
+  const uint32_t gm = min(m_tiles - band * g, band);
+  n = w / gm;
+  m = band * g + (w - n * gm);
+}
+
 // Eight neighbouring 16-bit floats of a row that ends at K; rows may start at
 // any multiple of 2 bytes.
 __device__ __forceinline__ u32x4_t load_piece(const uint16_t* p, int k, int K) {

@@ -1,5 +1,5 @@
-// Products of 8-bit tokens with 8-bit weights for many tokens (i8_linear.hip
-// has the formula and the form for few).
+// Products of 8-bit tokens with 8-bit weights in large tiles (i8_linear.hip has
+// the formula, the form in small ones and the choice).
 //
 // A block of four waves has a tile of 128 NI weight rows and 32 JT tokens; wave
 // w has 32 NI of the rows against all the tokens, NI x JT accumulators of the
@@ -39,19 +39,6 @@ constexpr int wait_imm(int vm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4)
 __device__ __forceinline__ i32x16_t mfma32(u32x4_t a, u32x4_t b, i32x16_t c) {
   return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a),
                                                __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
-}
-
-// The tile of a block.  Blocks go to the eight XCDs in turn; neighbouring ranks
-// are made to be on one, whose L2 then holds what they share.  Ranks walk bands
-// of 1024 tokens, a column of tiles of the band at a time.
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t total, uint32_t m_tiles,
-                                        uint32_t n_tiles, uint32_t band, uint32_t& m, uint32_t& n) {
-  const uint32_t xcd = id % 8, per = total / 8, extra = total % 8;
-  const uint32_t rank = xcd * per + min(xcd, extra) + id / 8;
-  const uint32_t span = band * n_tiles, g = rank / span, w = rank - g * span;
-  const uint32_t gm = min(m_tiles - band * g, band);
-  n = w / gm;
-  m = band * g + (w - n * gm);
 }
 
 // A wave's outputs: RO rows from n0 on of the 32 J tokens from m0 on.  All of
@@ -153,8 +140,8 @@ void gemm_i8_kernel(I8LinearArg p) {
   const int lr = lane & 31, lg = lane >> 5;
   const int64_t Kp = i8_padded(p.K), n_panels = (p.N + 15) / 16;
   uint32_t mt, nt;
-  tile_of(blockIdx.x, gridDim.x, (uint32_t)((p.M + TM - 1) / TM), (uint32_t)((p.N + TN - 1) / TN),
-          1024 / TM, mt, nt);
+  i8_tile_of(blockIdx.x, gridDim.x, (uint32_t)((p.M + TM - 1) / TM),
+             (uint32_t)((p.N + TN - 1) / TN), 1024 / TM, mt, nt);
   const int64_t m0 = (int64_t)mt * TM, n0 = (int64_t)nt * TN;
   // x of tile kt + 2 has to be there at the end of iteration kt, and is when
   // no more operations are outstanding than came behind it: those of ST - 3
@@ -292,48 +279,16 @@ void go(const I8LinearArg& p, hipStream_t s) {
   gemm_i8_kernel<DT, NI, JT, G><<<dim3((unsigned)blocks), 256, 0, s>>>(p);
 }
 
-// Which tile.  What a tile of K (128 columns) takes, in us, as measured (gfx950,
-// 2.35 GHz while the chip is not at its power limit): `busy` for each block that
-// a CU has when all have some, `alone` for a block when most CUs have none.  Of
-// a call with B blocks that is the larger of busy B / 256 and alone ceil(B /
-// 256), for the CU that has most.  Small tiles give more blocks, large ones read
-// less: 501 tokens, N 4096, K 4096 take 13.2 us with 64 x 128, 15.7 with 128 x
-// 128, 16.7 with 32 x 128 and 23.9 with 128 x 256; 1000 tokens, N and K 8192 take
-// 85, 64, 120 and 60.  A tile of 256 x 256 gained 2 % at 8192^3 and nothing at
-// 4096 x 22016 x 8192; splitting K over blocks, with a join in a second launch,
-// gained 3 % in the latter's last round and lost elsewhere (501 tokens 22 us, 2048
-// tokens of N 4096, K 11008 92 against 85).
-struct Tile {
-  int tm, tn;
-  float busy, alone;
-};
-constexpr Tile kPlain[] = {{32, 128, 0.225f, 0.12f}, {64, 128, 0.27f, 0.2f},
-                           {128, 128, 0.48f, 0.33f}, {128, 256, 0.83f, 0.59f}};
-constexpr Tile kGated[] = {{32, 128, 0.43f, 0.25f}, {64, 128, 0.52f, 0.35f}, {128, 128, 0.88f, 0.59f}};
-template <int C>
-int best_of(const Tile (&tiles)[C], int64_t M, int64_t N) {
-  int best = 0;
-  float least = 0.0f;
-  for (int i = 0; i < C; ++i) {
-    const Tile& t = tiles[i];
-    const int64_t blocks = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn);
-    const float a = t.busy * (float)blocks / 256.0f, b = t.alone * (float)((blocks + 255) / 256);
-    const float time = a > b ? a : b;
-    if (i == 0 || time < least) best = i, least = time;
-  }
-  return best;
-}
-
 template <class DT, int G>
-void pick(const I8LinearArg& p, hipStream_t s) {
+void pick(const I8LinearArg& p, int tile, hipStream_t s) {
   if constexpr (G == 2) {
-    switch (best_of(kGated, p.M, p.N)) {
+    switch (tile) {
       case 0: return go<DT, 2, 1, 2>(p, s);
       case 1: return go<DT, 2, 2, 2>(p, s);
       default: return go<DT, 2, 4, 2>(p, s);
     }
   } else {
-    switch (best_of(kPlain, p.M, p.N)) {
+    switch (tile) {
       case 0: return go<DT, 1, 1, 1>(p, s);
       case 1: return go<DT, 1, 2, 1>(p, s);
       case 2: return go<DT, 1, 4, 1>(p, s);
@@ -344,17 +299,17 @@ void pick(const I8LinearArg& p, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_gemm_i8(const I8LinearArg& p, bool f16, hipStream_t s) {
+hipError_t launch_gemm_i8(const I8LinearArg& p, int tile, bool f16, hipStream_t s) {
   if (p.tiles[1]) {
     if (f16)
-      pick<F16T, 2>(p, s);
+      pick<F16T, 2>(p, tile, s);
     else
-      pick<Bf16T, 2>(p, s);
+      pick<Bf16T, 2>(p, tile, s);
   } else {
     if (f16)
-      pick<F16T, 1>(p, s);
+      pick<F16T, 1>(p, tile, s);
     else
-      pick<Bf16T, 1>(p, s);
+      pick<Bf16T, 1>(p, tile, s);
   }
   return hipGetLastError();
 }

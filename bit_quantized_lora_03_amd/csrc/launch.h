@@ -285,7 +285,8 @@ struct I8LinearArg {
   int act;  // kI8Silu or kI8Gelu (i8_common.h)
 };
 hipError_t launch_linear_i8(const I8LinearArg& p, bool f16, hipStream_t s);
-// i8_gemm.hip -- its form for many tokens
-hipError_t launch_gemm_i8(const I8LinearArg& p, bool f16, hipStream_t s);
+// i8_gemm.hip -- its form in large tiles: 0 .. 3 are 32, 64 and 128 tokens by 128
+// rows and 128 by 256 (0 .. 2 for two weights)
+hipError_t launch_gemm_i8(const I8LinearArg& p, int tile, bool f16, hipStream_t s);
 
 }  // namespace qlora
