@@ -118,8 +118,10 @@ struct Outputs {
   }
 };
 
+// Up to four blocks of the small tiles on a CU: 2048 tokens of 8192 x 128 take
+// 16.5 us, 17.7 with two, gated 785 of 10016 x 333 18.9 and 20.7.
 template <class DT, int NI, int JT, int G>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2)))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, JT <= 2 ? 4 : 2)))
 void gemm_i8_kernel(I8LinearArg p) {
   using S = Outputs<DT, NI, G, JT>;
   constexpr int TM = 32 * JT, RO = S::RO, TN = 4 * RO;
