@@ -19,6 +19,7 @@ from .u4 import _16BIT, _call, _dense, _need
 PAD = 128
 ACTS = {"silu": 0, "gelu": 1}
 _i8, _f32 = torch.int8, torch.float32
+_empty = torch.empty  # (0.3 us less a call with the sizes as arguments than as a tuple)
 
 
 def _padded(K: int) -> int:
@@ -108,8 +109,8 @@ class I8Tokens:
         """Room for ``M`` tokens, uninitialised."""
         if K < 1:
             raise ValueError(f"K = {K}: tokens have at least one value")
-        codes = torch.empty((M, (K + 127) // 128 * 128), dtype=_i8, device=device)
-        scales = torch.empty((M,), dtype=_f32, device=device)
+        codes = _empty(M, (K + 127) // 128 * 128, dtype=_i8, device=device)
+        scales = _empty(M, dtype=_f32, device=device)
         index = codes.get_device()
         if index < 0:
             raise ValueError(f"tokens on the GPU are needed, not on {codes.device}")
@@ -164,7 +165,7 @@ def dequantize_i8(iw: I8Weight, dtype=torch.bfloat16):
     """I8Weight -> its values [N, K] in bf16 or fp16."""
     _need(dtype in _16BIT, "bf16 or fp16 values")
     w = iw.now()
-    out = torch.empty((iw.N, iw.K), dtype=dtype, device=iw.device)
+    out = _empty(iw.N, iw.K, dtype=dtype, device=iw.device)
     _call("qlora_dequantize_i8", dtype, iw.index, w, out.data_ptr())
     return out
 
@@ -188,7 +189,7 @@ def dequantize_tokens_i8(t: I8Tokens, dtype=torch.bfloat16):
     """I8Tokens -> their values [M, K] in bf16 or fp16."""
     _need(dtype in _16BIT, "bf16 or fp16 values")
     s = t.now()
-    out = torch.empty((t.M, t.K), dtype=dtype, device=t.device)
+    out = _empty(t.M, t.K, dtype=dtype, device=t.device)
     _call("qlora_dequantize_tokens_i8", dtype, t.index, s, out.data_ptr())
     return out
 
@@ -217,7 +218,7 @@ def rms_norm_i8(x, weight, eps: float, residual=None, h=None, out=None):
         ldr = _rows(residual, "residual", dt, M, K, index)
         rp = residual.data_ptr()
         if h is None:
-            h, ldh = torch.empty((M, K), dtype=dt, device=x.device), K
+            h, ldh = _empty(M, K, dtype=dt, device=x.device), K
         else:
             ldh = _rows(h, "h", dt, M, K, index)
         hp = h.data_ptr()
@@ -250,7 +251,7 @@ def _place(w: I8Weight, x: I8Tokens, y, dtype):
     if dtype not in _16BIT:
         raise ValueError("bf16 or fp16 outputs")
     if y is None:
-        return torch.empty((M, N), dtype=dtype, device=x.device), dtype, N
+        return _empty(M, N, dtype=dtype, device=x.device), dtype, N
     return y, dtype, ld
 
 
