@@ -631,7 +631,8 @@ int qlora_linear_i8_fwd_f16(const qlora_i8_weight* w, const qlora_i8_tokens* x, 
 /* The gated half of an MLP: y = act(g) * u with g = x . gate^T and
  * u = x . up^T (weights of one shape, EINVAL), in one pass; g and u are fp32
  * and never rounded to 16 bits; a factor 1 / (1 + exp) below 2^-126 counts
- * as 0.  act (ENOTSUP for others):
+ * as 0.  The same bits on every run and for every M.  act (ENOTSUP for
+ * others):
  *   QLORA_ACT_SILU  g / (1 + exp(-g))
  *   QLORA_ACT_GELU  the tanh form, g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
  * Other arguments as above.                                                  */

@@ -328,11 +328,11 @@ def test_product(cuda, M, N, K, dtype):
     assert torch.equal(q.linear_i8_fwd(iw, t, dtype=tdtype(dtype)), y.t)
 
 
-# each of the tiles, at its edges: 32 x 128, 64 x 128, 128 x 128, 128 x 256,
-# with K of one tile and of even and odd numbers of them
-WIDE = [(17, 4096, 128), (20, 5000, 300), (32, 4097, 200), (33, 4000, 100), (97, 11000, 130), (130, 8192, 257), (200, 11008, 300), (230, 10900, 384),
-        (500, 4096, 513), (501, 4091, 128), (700, 8192, 200), (1025, 8200, 256), (2047, 5001, 640),
-        (3000, 2053, 1111)]
+# the larger tiles, at their edges: 32 x 32, 32 x 128, 64 x 128, 128 x 128,
+# 128 x 256, with K of one tile and of even and odd numbers of them
+WIDE = [(17, 4096, 128), (20, 5000, 300), (32, 4097, 200), (33, 4000, 100), (97, 11000, 130),
+        (130, 8192, 257), (200, 11008, 300), (230, 10900, 384), (500, 4096, 513),
+        (501, 4091, 128), (700, 8192, 200), (1025, 8200, 256), (2047, 5001, 640), (3000, 2053, 1111)]
 
 
 @TYPES
@@ -479,7 +479,7 @@ def gated_ref(cx, sx, cg, sg, cu, su, act):
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 100, 300), (4, 1000, 128), (16, 35, 2000),
                                    (30, 64, 640), (64, 200, 1000), (65, 130, 512), (128, 128, 256),
                                    (200, 300, 1500), (300, 513, 1024), (520, 260, 700),
-                                   # each of the tiles: 32, 64 and 128 tokens
+                                   # more rows: small and large tiles
                                    (33, 5000, 300), (100, 11008, 140), (301, 11000, 130),
                                    (1030, 4096, 257)])
 def test_gated(cuda, M, N, K, act, dtype):
@@ -720,7 +720,7 @@ def test_a_block_runs_together(cuda, M, dtype):
     assert float((h.double() - wh.double()).norm() / wh.double().norm()) <= bar
 
 
-@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("M", [1, 40, 300, 2000])
 def test_captured_and_replayed(cuda, M):
     """A captured block, replayed with other inputs in the same places, gives
     the eager call's bits; eager work runs between the replays."""

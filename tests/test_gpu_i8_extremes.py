@@ -142,3 +142,29 @@ def test_longest_rows(cuda):
         assert np.array_equal(t.codes.cpu().numpy(), c)
         y = q.linear_i8_fwd(iw, t, dtype=torch.float16)
         assert np.array_equal(bits(y), round16(scaled(i8.sums(c, cw), sw, t.scales.cpu().numpy()), "f16"))
+
+
+@pytest.mark.parametrize("M,N", [(60, 4096), (60, 8191), (40, 11000), (150, 8192), (701, 4099), (2000, 8192)])
+def test_longest_rows_in_every_tile(cuda, M, N):
+    """K = 2^17 - 128 against enough rows for the larger tiles, 32 x 32 to 128 x
+    256: codes of all values, and -128 throughout, whose sums are 2^31 - 2^21."""
+    import torch
+    torch.manual_seed(M)
+    K = (1 << 17) - 128
+    tiles, codes = random_codes((N + 15) // 16, K // 64, 4, 16, 16), random_codes(M, K)
+    w = q.I8Weight(tiles, torch.rand(N, device="cuda") + 0.5, N, K)
+    t = q.I8Tokens(codes, torch.rand(M, device="cuda") + 0.5, K)
+    y = q.linear_i8_fwd(w, t)
+    rows = [0, 1, M // 2, M - 1]
+    cx, sx = codes[rows].cpu().numpy(), t.scales[rows].cpu().numpy()
+    for first in (0, N // 32 * 16, (N - 1) // 16 * 16):
+        n = min(16, N - first)
+        cw = tiles[first // 16].cpu().numpy().transpose(2, 0, 1, 3).reshape(16, K)[:n]
+        sw = w.scales[first:first + n].cpu().numpy()
+        want = round16(scaled(i8.sums(cx, cw), sw, sx), "bf16")
+        assert np.array_equal(bits(y[rows][:, first:first + n]), want)
+    tiles.fill_(-128)
+    codes.fill_(-128)
+    w.scales.fill_(0.5)
+    t.scales.fill_(1.0)
+    assert (q.linear_i8_fwd(w, t) == float(np.float32(K << 14)) * 0.5).all()
