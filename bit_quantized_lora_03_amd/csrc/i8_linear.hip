@@ -155,16 +155,16 @@ __global__ __launch_bounds__(64 * W) void few_i8_kernel(I8LinearArg p) {
 //   start + max(ceil(B / 256) alone k, B / 256 (busy k + end))   us
 //
 // with what a tile of K takes in the CU that has most blocks, or in all of them
-// when they have many, and what a block's outputs take; fitted to 560 calls
-// (1 to 4000 tokens, 16 to 22016 rows, K to 11008), each timed in every form:
-// the chosen one is within 0.4 % of the best in the mean and 10 % in the worst.
-// Without 16 x 16 calls take 5 to 7 % more in the mean, without any other 0.7 to
-// 4 %.  A few: 256 tokens of 1024 x 8192 take 7.6
-// us in 32 x 32, 12.2 in 16 x 16 and 13.4 in 32 x 128; 61 of 11008 x 4096 10.5
-// in 32 x 128 and 12.0 in 32 x 32; 501 of 4096 x 4096 12.5 in 64 x 128, 15.7 in
-// 128 x 128 and 18.8 in 64 x 32; 1000 of 8192 x 8192 85, 64, 120 and 60 in the
-// large tiles, smallest first.  A tile of 256 x 256 gained 2 % at 8192^3 and
-// nothing at 4096 x 22016 x 8192; splitting K over blocks, with a join in a
+// when they have many, and what a block's outputs take; fitted to 560 calls (1
+// to 4000 tokens, 16 to 22016 rows, K to 11008), each timed in every form.  In
+// 440 other calls the chosen one is within 0.4 % of the best in the mean and 20 %
+// in the worst (1428 tokens of 11008 x 320).  Without 16 x 16 calls take 5 to 7 %
+// more in the mean, without any other form 0.7 to 4 %.  256 tokens of 1024 x 8192
+// take 7.3 us in 32 x 32, 12.2 in 16 x 16 and 13.4 in 32 x 128; 61 of 11008 x
+// 4096 10.5 in 32 x 128 and 12.0 in 32 x 32; 501 of 4096 x 4096 12.5 in 64 x 128,
+// 15.7 in 128 x 128 and 18.8 in 64 x 32; 1000 of 8192 x 8192 85, 64, 120 and 60
+// in the large tiles, smallest first.  A tile of 256 x 256 gained 2 % at 8192^3
+// and nothing at 4096 x 22016 x 8192; splitting K over blocks, with a join in a
 // second launch, gained 3 % in the latter's last round and lost elsewhere.
 struct Form {
   int tm, tn;
