@@ -9,12 +9,13 @@
 //
 // Bound by HBM.  A row stays in registers between the two passes, so each
 // input is read once.  A row of up to 2048 values belongs to one wave (no
-// barrier), up to 16384 to four, longer ones to sixteen.  Sums, maxima and
+// barrier; where rows are few, of up to 512 values), up to 16384 to four, longer
+// ones to sixteen.  Sums, maxima and
 // quotients are fp64: with a product of two 16-bit floats exact in it nothing
 // overflows, and its share is small beside the memory's.
 //
-// Measured: 4096 tokens of 8192 20 us, with the norm and a residual 47 (5.0 TB/s;
-// a large copy 5.16); 2047 of 11008 16.1 and 41; one of 4096 2.5 and 3.9 in a
+// Measured: 4096 tokens of 8192 20 us, with the norm and a residual 46 (5.1 TB/s;
+// a large copy 5.16); 2047 of 11008 16.1 and 41; one of 4096 2.5 and 3.6 in a
 // replayed graph.
 
 #include <type_traits>
@@ -46,15 +47,32 @@ __global__ __launch_bounds__(rows_threads<W>()) void rows_i8_kernel(I8RowsArg p)
   };
   const int64_t row = (int64_t)blockIdx.x * ROWS + (W == 1 ? wave : 0);
   if (row >= p.M) return;
-  // The weight is read anew for each pass, or its values and products would
-  // be kept as fp64 over passes and rows, and spilled.
+  // The norm's weight: up to four pieces a lane are asked for with x and held
+  // (one token of 4096 3.9 -> 3.6 us, of 8192 5.4 -> 4.9; 2047 of 4096 17.3 ->
+  // 15.8), more are read anew for each pass.  Either way it is opaque to the last
+  // pass, or its values and products would be kept as fp64 and spilled.
+  constexpr bool kHeld = NORM && CH <= 4;
   const uint16_t* pw = p.w;
   asm volatile("" : "+s"(pw));
   u32x4_t h[CH];
   const uint16_t* x = p.x + row * p.ldx;
 #pragma unroll
   for (int i = 0; i < CH; ++i) h[i] = load_piece(x, 8 * (i * T + at), K);
-  double a = 0.0, sum = 0.0;
+  u32x4_t held[kHeld ? CH : 1];
+  if constexpr (kHeld) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) held[i] = load_piece(pw, 8 * (i * T + at), K);
+  }
+  auto weight = [&](int i) {
+    if constexpr (kHeld)
+      return held[i];
+    else
+      return load_piece(pw, 8 * (i * T + at), K);
+  };
+  // One wave sums its pieces of 64 lanes apart and joins them as four waves do, so
+  // a row's bits do not depend on which of them has it.
+  constexpr int NS = W == 1 ? CH : 1;
+  double a = 0.0, sum = 0.0, s[NS] = {};
   uint32_t top = 0;
   bool ok = true;
   if constexpr (NORM) {
@@ -77,12 +95,12 @@ __global__ __launch_bounds__(rows_threads<W>()) void rows_i8_kernel(I8RowsArg p)
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const u32x4_t w = load_piece(pw, 8 * (i * T + at), K);
+      const u32x4_t w = weight(i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const double v = DT::tof((uint16_t)half_of(h[i], j));
         const double t = fabs(v * DT::tof((uint16_t)half_of(w, j)));
-        sum = __builtin_fma(v, v, sum);
+        s[i % NS] = __builtin_fma(v, v, s[i % NS]);
         a = fmax(a, t);
         ok = ok && t <= 1e300;
       }
@@ -91,8 +109,11 @@ __global__ __launch_bounds__(rows_threads<W>()) void rows_i8_kernel(I8RowsArg p)
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) {
       a = fmax(a, lane_xor(a, m));
-      sum += lane_xor(sum, m);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) s[i] += lane_xor(s[i], m);
     }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) sum += s[i];
     ok = __all(ok);
   } else {
 #pragma unroll
@@ -131,10 +152,13 @@ __global__ __launch_bounds__(rows_threads<W>()) void rows_i8_kernel(I8RowsArg p)
   asm volatile("" : "+s"(pw));
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    if constexpr (NORM) asm volatile("" : "+v"(h[i]));
     const int k = 8 * (i * T + at);
     u32x4_t w;
-    if constexpr (NORM) w = load_piece(pw, k, K);
+    if constexpr (NORM) {
+      asm volatile("" : "+v"(h[i]));
+      if constexpr (kHeld) asm volatile("" : "+v"(held[i]));
+      w = weight(i);
+    }
     u32x2_t c = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -172,6 +196,12 @@ void go_rows(const I8RowsArg& p, hipStream_t s) {
   // as many pieces a lane as a row has use for (with powers of two alone 2047
   // rows of 11008 took 17.5 us where they take 16.1, the norm 44.4 and 41.1)
   QLORA_I8_ROWS(1, 1);
+  // few rows of up to 2048 values are done sooner by four waves (one of 2048 2.6
+  // -> 2.2 us, with the norm 4.3 -> 3.1; 512 3.2 -> 3.0 and 5.3 -> 4.4; 1024 3.5
+  // -> 3.9 and 5.9 -> 6.2)
+  if (p.M <= 512) {
+    QLORA_I8_ROWS(4, 1);
+  }
   QLORA_I8_ROWS(1, 2);
   QLORA_I8_ROWS(1, 3);
   QLORA_I8_ROWS(1, 4);

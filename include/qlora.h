@@ -609,7 +609,8 @@ int qlora_dequantize_tokens_i8_f16(const qlora_i8_tokens* t, uint16_t* out, void
  *   weight [K] of the same type.  h is written where residual is given and
  *   has to be NULL otherwise (EINVAL); it may be x or residual itself (the
  *   same address and row distance), no other overlap.
- *   eps >= 0 and finite (EINVAL).  Sums, products and quotients are fp64.
+ *   eps >= 0 and finite (EINVAL).  Sums, products and quotients are fp64, a
+ *   row's the same bits on every run and for every M.
  * A row of zeros has scale 0 with any eps > 0, and NaN with eps = 0.        */
 int qlora_rms_norm_i8(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
                       const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* h,

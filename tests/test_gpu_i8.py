@@ -241,6 +241,30 @@ def test_norm(cuda, K, residual, dtype):
 
 
 @TYPES
+@pytest.mark.parametrize("K", [513, 1000, 1024, 1500, 2048])
+def test_many_rows_and_the_same_alone(cuda, K, dtype):
+    """Rows whose squares fp64 does not add exactly: the same bits in 600 rows,
+    which a wave has each, as alone."""
+    import torch
+    x, v = activations(600, K, dtype, K, spread=3.0 if dtype == "f16" else 20.0)
+    x = torch.where(x.isinf(), torch.ones_like(x), x)
+    r = activations(600, K, dtype, K + 1)[0]
+    w = (1 + 0.1 * activations(1, K, dtype, 9)[0])[0].contiguous()
+    for norm in (False, True):
+        f = (lambda a, b: q.rms_norm_i8(a, w, 1e-5, residual=b)[0]) if norm else \
+            (lambda a, b: q.quantize_tokens_i8(a))
+        many = f(x, r)
+        for i in (0, 3, 301, 599):
+            one = f(x[i:i + 1], r[i:i + 1])
+            assert torch.equal(one.codes[0], many.codes[i]) and torch.equal(one.scales[0], many.scales[i])
+    t, h = q.rms_norm_i8(x, w, 1e-5, residual=r)
+    check_norm(t, f64(h), f64(w), 1e-5)
+    c, sc = i8.encode(f64(x))
+    t = q.quantize_tokens_i8(x)
+    assert np.array_equal(t.codes.cpu().numpy(), i8.pad(c)) and np.array_equal(t.scales.cpu().numpy(), sc)
+
+
+@TYPES
 def test_norm_special_rows(cuda, dtype):
     """Zeros, infinities, NaN, and rows whose squares fp32 does not hold."""
     import torch
