@@ -9,14 +9,14 @@
 //
 // Bound by HBM.  A row stays in registers between the two passes, so each
 // input is read once.  A row of up to 2048 values belongs to one wave (no
-// barrier; where rows are few, of up to 512 values), up to 16384 to four, longer
-// ones to sixteen.  Sums, maxima and
-// quotients are fp64: with a product of two 16-bit floats exact in it nothing
-// overflows, and its share is small beside the memory's.
+// barrier; where rows are few, of up to 512 values), longer ones to four, eight
+// or sixteen.  Sums, maxima and quotients are fp64: with a product of two 16-bit
+// floats exact in it nothing overflows, and its share is small beside the
+// memory's.
 //
 // Measured: 4096 tokens of 8192 20 us, with the norm and a residual 46 (5.1 TB/s;
-// a large copy 5.16); 2047 of 11008 16.1 and 41; one of 4096 2.5 and 3.6 in a
-// replayed graph.
+// a large copy 5.16); 2047 of 11008 16.1 and 37, of 22016 27 and 72; one of 4096
+// 2.5 and 3.6 in a replayed graph.
 
 #include <type_traits>
 
@@ -193,8 +193,11 @@ void go_rows(const I8RowsArg& p, hipStream_t s) {
 #define QLORA_I8_ROWS(W, CH) \
   if (pieces <= 64 * (W) * (CH)) \
     return run(rows_i8_kernel<DT, W, CH, NORM>, rows_threads<W>(), (W) == 1 ? 4 : 1)
-  // as many pieces a lane as a row has use for (with powers of two alone 2047
-  // rows of 11008 took 17.5 us where they take 16.1, the norm 44.4 and 41.1)
+  // as many pieces a lane as a row has use for: with powers of two alone 2047
+  // rows of 11008 took 17.5 us where they take 16.1.  More waves and fewer pieces
+  // where the norm would hold too much: 2047 of 11008 36 to 38 us, 41 with
+  // four waves of six pieces (without the norm 16.9 and 16.0); of 22016 72 us, and 27 without
+  // it, 97 and 31 with sixteen waves of three, which leave a CU one row.
   QLORA_I8_ROWS(1, 1);
   // few rows of up to 2048 values are done sooner by four waves (one of 2048 2.6
   // -> 2.2 us, with the norm 4.3 -> 3.1; 512 3.2 -> 3.0 and 5.3 -> 4.4; 1024 3.5
@@ -208,11 +211,17 @@ void go_rows(const I8RowsArg& p, hipStream_t s) {
   QLORA_I8_ROWS(4, 2);
   QLORA_I8_ROWS(4, 3);
   QLORA_I8_ROWS(4, 4);
-  QLORA_I8_ROWS(4, 5);
-  QLORA_I8_ROWS(4, 6);
-  QLORA_I8_ROWS(4, 8);
-  QLORA_I8_ROWS(16, 3);
-  QLORA_I8_ROWS(16, 4);
+  if constexpr (NORM) {
+    QLORA_I8_ROWS(8, 3);
+    QLORA_I8_ROWS(8, 4);
+  } else {
+    QLORA_I8_ROWS(4, 5);
+    QLORA_I8_ROWS(4, 6);
+    QLORA_I8_ROWS(4, 8);
+  }
+  QLORA_I8_ROWS(8, 5);
+  QLORA_I8_ROWS(8, 6);
+  QLORA_I8_ROWS(8, 8);
   QLORA_I8_ROWS(16, 6);
   QLORA_I8_ROWS(16, 8);
   QLORA_I8_ROWS(16, 16);

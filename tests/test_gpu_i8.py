@@ -146,8 +146,8 @@ def test_quantize_weight_writes_nothing_else(cuda):
 # tokens
 # ---------------------------------------------------------------------------
 
-WIDTHS = [1, 7, 8, 127, 128, 129, 500, 512, 513, 1024, 2048, 2056, 4096, 4097, 8192, 11008, 16384,
-          16392, 22016, 32768, 40001, 65544, 130944]
+WIDTHS = [1, 7, 8, 127, 128, 129, 500, 512, 513, 1024, 2048, 2056, 4096, 4097, 8192, 9001, 11008,
+          13000, 16384, 16392, 22016, 32768, 40001, 50000, 65544, 130944]
 
 
 @TYPES
