@@ -195,9 +195,9 @@ void go_rows(const I8RowsArg& p, hipStream_t s) {
     return run(rows_i8_kernel<DT, W, CH, NORM>, rows_threads<W>(), (W) == 1 ? 4 : 1)
   // as many pieces a lane as a row has use for: with powers of two alone 2047
   // rows of 11008 took 17.5 us where they take 16.1.  More waves and fewer pieces
-  // where the norm would hold too much: 2047 of 11008 36 to 38 us, 41 with
-  // four waves of six pieces (without the norm 16.9 and 16.0); of 22016 72 us, and 27 without
-  // it, 97 and 31 with sixteen waves of three, which leave a CU one row.
+  // where the norm would hold too much: 2047 of 11008 36 to 38 us, 41 with four
+  // waves of six pieces (without the norm 16.9 and 16.0); of 22016 72 us, and 27
+  // without it, 97 and 31 with sixteen waves of three, which leave a CU one row.
   QLORA_I8_ROWS(1, 1);
   // few rows of up to 2048 values are done sooner by four waves (one of 2048 2.6
   // -> 2.2 us, with the norm 4.3 -> 3.1; 512 3.2 -> 3.0 and 5.3 -> 4.4; 1024 3.5
