@@ -24,12 +24,14 @@ __host__ __device__ __forceinline__ int64_t i8_padded(int64_t K) {
   return (K + kI8Pad - 1) & ~(int64_t)(kI8Pad - 1);
 }
 
-// How a row is coded.  The quotient 127 v / a decides borders exactly: v and
-// a have at most 24 significant bits, or 22 as products of two 16-bit floats,
-// so a quotient that is no half has a distance of 2^-26 of itself and more
-// from any, and a half comes out as it is: q below is the quotient rounded
-// once (r is off by an ulp at most, and one correction in exact arithmetic
-// follows).
+// How a row is coded.  The quotient 127 v / a decides borders exactly: it
+// differs from h / 2, h odd, by |254 v - h a| / (h a) of it, and with v = V 2^e
+// and a = A 2^f the difference is a multiple of 2^f (then 1 / (h A) at least) or
+// an even one of 2^e (1 / (127 V)).  V and A are below 2^24, or 2^22 as products
+// of two 16-bit floats, and h is at most 253, so a quotient that is no half is
+// more than 2^-32 of itself away from any (2^-30); some come that close.  A half
+// comes out as it is: q below is the quotient rounded once (r is off by an ulp at
+// most, and one correction in exact arithmetic follows).
 struct I8Row {
   double a, r;  // r = 1 / a, or 0 for a row of zeros
   float s;
