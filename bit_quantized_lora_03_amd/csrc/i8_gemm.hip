@@ -16,13 +16,14 @@
 // its number ^ (row / 2) % 8, so the 16 rows that a read serves in a cycle lie
 // in different banks.
 //
-// Large calls are bound by the chip's power: the loop keeps the matrix cores busy
-// for 93 % of the cycles where few CUs work, 80 % on a full chip, whose clock is
-// then 1.3 to 1.7 GHz instead of 2.35.  8192^3: 425 to 430 us, 2570 TOPS (the
-// library's int8 product 2425 to 2473); 4096 tokens of 22016 x 8192 587 to 596
-// us; gated, 2047 of 11008 x 4096, 160 to 168.  501 tokens of 4096 x 4096 (12.4 us)
-// are bound by L2, which gives 21 TB/s; 61 of 11008 x 4096 (10.2) by the weight's
-// way from behind it.
+// Large calls are bound by the chip's power: the matrix cores are busy for 80 %
+// of the cycles in 128 x 256 (4096 tokens of 22016 x 8192) and for 64 % in the
+// gated 128 x 128 (2047 of 11008 x 4096), on a full chip whose clock is then 1.3
+// and 1.7 GHz instead of 2.35.  Once a run is under way 8192^3 takes 419 to 449 us
+// by the codes, 2450 to 2620 TOPS (the library's int8 product of the same codes
+// 439 to 447); 4096 tokens of 22016 x 8192 587 to 606 us (715 to 726); gated, 2047
+// of 11008 x 4096, 159 to 168.  501 tokens of 4096 x 4096 (12.4 us) are bound by L2,
+// which gives 21 TB/s; 61 of 11008 x 4096 (10.2) by the weight's way from behind it.
 
 #include "i8_common.h"
 #include "launch.h"
@@ -44,8 +45,8 @@ __device__ __forceinline__ i32x16_t mfma32(u32x4_t a, u32x4_t b, i32x16_t c) {
 // A wave's outputs: RO rows from n0 on of the 32 J tokens from m0 on.  All of
 // them are scaled into the wave's LDS first, and go out from there in a loop,
 // in runs of a token's row: done for 32 tokens at a time, with a wait between
-// each write and read and code for every one, it took 10 us a tile of 256 x
-// 256, a tenth of the time at K 8192.
+// each write and read and code for every one, it took 10 us a tile of 256 x 256
+// (the largest when this was measured, now gone), a tenth of the time at K 8192.
 template <class DT, int NI, int G, int J>
 struct Outputs {
   static constexpr int RO = G == 2 ? 32 : 32 * NI;
