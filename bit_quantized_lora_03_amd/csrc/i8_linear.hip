@@ -46,10 +46,10 @@ constexpr int W = 8;  // waves of a block
 // Bound by HBM on the weights where tokens are few: 1 token of 4096 x 4096 takes
 // 3.4 us in a replayed graph (a copy of the bytes 3.3), 16 of 8192 x 8192 11.9
 // (13.1, but part stays in the last-level cache), 4 of a gated 11008 x 4096 15.3
-// (17.5), 4 of 22016 x 8192 26.9; else by what a CU takes in, 120 GB/s of its
-// tile, up to 25 TB/s for all (256 of 1024 x 8192 7.3, 32 of 4096 x 4096 4.3).
-// Neither two tiles of K in flight nor loads ahead of the exchange through LDS
-// gained anything.
+// (17.5), 4 of 22016 x 8192 26.9; else by what a CU takes in of its tile (32 of
+// 4096 x 4096 4.3; 256 of 1024 x K, a block of 32 x 32 on each CU, 4.3 at K 2048
+// and 7.5 at 8192: 123 GB/s a CU, 31 TB/s for all, from L2).  Neither two tiles of
+// K in flight nor loads ahead of the exchange through LDS gained anything.
 template <class DT, int G, int T, int R>
 __global__ __launch_bounds__(64 * W) void few_i8_kernel(I8LinearArg p) {
   constexpr int KT = 128;                               // columns at a time
@@ -155,8 +155,9 @@ __global__ __launch_bounds__(64 * W) void few_i8_kernel(I8LinearArg p) {
 //   start + max(ceil(B / 256) alone k, B / 256 (busy k + end))   us
 //
 // with what a tile of K takes in the CU that has most blocks, or in all of them
-// when they have many, and what a block's outputs take; fitted to 560 calls (1
-// to 4000 tokens, 16 to 22016 rows, K to 11008), each timed in every form.  In
+// when they have many, and what a block's outputs take; fitted together, for the
+// choice (one alone is no rate), to 560 calls (1 to 4000 tokens, 16 to 22016
+// rows, K to 11008), each timed in every form.  In
 // 440 other calls the chosen one is within 0.4 % of the best in the mean and 20 %
 // in the worst (1428 tokens of 11008 x 320).  Without 16 x 16 calls take 5 to 7 %
 // more in the mean, without any other form 0.7 to 4 %.  256 tokens of 1024 x 8192
