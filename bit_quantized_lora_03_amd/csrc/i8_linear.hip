@@ -166,7 +166,9 @@ __global__ __launch_bounds__(64 * W) void few_i8_kernel(I8LinearArg p) {
 // 15.7 in 128 x 128 and 18.8 in 64 x 32; 1000 of 8192 x 8192 85, 64, 120 and 60
 // in the large tiles, smallest first.  A tile of 256 x 256 gained 2 % at 8192^3
 // and nothing at 4096 x 22016 x 8192; splitting K over blocks, with a join in a
-// second launch, gained 3 % in the latter's last round and lost elsewhere.
+// second launch, gained 3 % in the latter's last round and lost on other large
+// calls; a join in the same launch is not tried, nor any at 65 to 1200 tokens, where
+// calls are 1.1 to 5 times their floor (256 of 1024 x 4096 5.4 us, floor 1.1).
 struct Form {
   int tm, tn;
   float start, alone, busy, end;
