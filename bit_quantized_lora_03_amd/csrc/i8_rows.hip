@@ -16,7 +16,9 @@
 //
 // Measured: 4096 tokens of 8192 20 us, with the norm and a residual 46 (5.1 TB/s;
 // a large copy 5.16); 2047 of 11008 16.1 and 37, of 22016 27 and 72; one of 4096
-// 2.5 and 3.6 in a replayed graph.
+// 2.5 and 3.6 in a replayed graph.  4096 of 65536 155 and 460 (4.1 TB/s), of 130944
+// 336 and 940 (4.0); of 65544, where half of the lanes' pieces are empty, 222 and
+// 679 (2.8).
 
 #include <type_traits>
 
@@ -41,7 +43,9 @@ __global__ __launch_bounds__(rows_threads<W>()) void rows_i8_kernel(I8RowsArg p)
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int at = W == 1 ? lane : threadIdx.x;
   const int K = (int)p.K, Kp = (int)i8_padded(K);
-  // at most four pieces' loads are ahead of their use, or long rows spill
+  // at most four pieces' loads are ahead of their use, or long rows spill (with
+  // the norm, those past 65536 values do all the same: 14 registers, 60 bytes a
+  // lane)
   auto fence = [](int i) {
     if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
   };
