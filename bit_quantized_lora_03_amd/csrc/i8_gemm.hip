@@ -21,8 +21,8 @@
 // gated 128 x 128 (2047 of 11008 x 4096), on a full chip whose clock is then 1.3
 // and 1.7 GHz instead of 2.35.  Once a run is under way 8192^3 takes 419 to 449 us
 // by the codes, 2450 to 2620 TOPS (the library's int8 product of the same codes
-// 439 to 447); 4096 tokens of 22016 x 8192 587 to 606 us (715 to 726); gated, 2047
-// of 11008 x 4096, 159 to 168.  501 tokens of 4096 x K, a block of 64 x 128 on each
+// 439 to 447); 4096 tokens of 22016 x 8192 585 to 618 us (715 to 726); gated, 2047
+// of 11008 x 4096, 159 to 174.  501 tokens of 4096 x K, a block of 64 x 128 on each
 // CU, take 7.9 us at K 2048, 12.5 at 4096 and 22.6 at 8192: 80 GB/s a CU, 20 TB/s
 // for all.  That is not L2's limit, which gives the small tiles 31; what holds it is
 // not known.  61 of 11008 x 4096 (10.2) are bound by the weight's way from behind L2.
